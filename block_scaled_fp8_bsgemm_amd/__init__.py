@@ -17,6 +17,13 @@ library has not been built, importing the functions raises immediately.
   mxgemm_fp8(A, a_scale, B, b_scale, C=None, bands=1, band_stride=0)
   band_rowq_e4m3(parts, q=None, scale=None)
   mxq_e4m3(x, q=None, scale=None)
+  lora_plan(ids, n_adapters, plan=None)
+  lora_shrink(x, A, plan, H=None)
+  lora_expand(H, B, plan, base, out=None, scale=None, bands=1, band_stride=0)
+  bsgemm_fp8_lora(A, a_scale, B, b_scale, H, lora_B, ids, scale=None, C=None, bands=1,
+                  band_stride=0)
+  resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.0, beta=1.0,
+          eps=1e-6, quant=0, resid_out=None, z=None, q=None, q_scale=None)
 
 Tensors: e4m3 codes are uint8 (or torch.float8_e4m3fn, reinterpreted), bf16
 values are torch.bfloat16 (or int16/uint16 bit patterns), scales float32.
@@ -37,6 +44,7 @@ BS_OK, BS_ERR_INVALID, BS_ERR_UNSUPPORTED, BS_ERR_LAUNCH = 0, 1, 2, 3
 # every extern "C" symbol of include/bsgemm.h
 EXPORTS = ("bsgemm_fp8", "band_reduce", "rowq_e4m3", "rowdq_e4m3", "blockq_e4m3", "actq_e4m3",
            "mxgemm_fp8", "mxq_e4m3", "bprepack_e4m3", "bsgemm_fp8_pb", "band_rowq_e4m3",
+           "lora_plan", "lora_shrink", "lora_expand", "bsgemm_fp8_lora", "resnorm",
            "bs_status_str")
 
 _lib = None
@@ -68,8 +76,13 @@ def load():
     L.bprepack_e4m3.argtypes = [vp, vp, i64, i64, vp]
     L.bsgemm_fp8_pb.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, i64, vp]
     L.band_rowq_e4m3.argtypes = [ctypes.POINTER(vp), i32, vp, vp, i64, i64, vp]
-    for f in ("bsgemm_fp8", "band_reduce", "rowq_e4m3", "rowdq_e4m3", "blockq_e4m3", "actq_e4m3",
-              "mxgemm_fp8", "mxq_e4m3", "bprepack_e4m3", "bsgemm_fp8_pb", "band_rowq_e4m3"):
+    f32 = ctypes.c_float
+    L.lora_plan.argtypes = [vp, vp, i64, i64, vp]
+    L.lora_shrink.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, vp]
+    L.lora_expand.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i64, vp]
+    L.bsgemm_fp8_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i64, vp]
+    L.resnorm.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i32, i32, f32, f32, f32, vp]
+    for f in EXPORTS[:-1]:
         getattr(L, f).restype = ctypes.c_int
     L.bs_status_str.argtypes = [ctypes.c_int]
     L.bs_status_str.restype = ctypes.c_char_p
@@ -351,3 +364,188 @@ def band_rowq_e4m3(parts, q=None, scale=None, stream=None):
                                rows, N, _stream(stream))
     _check(st, "band_rowq_e4m3")
     return q, scale
+
+
+def _here(name, *tensors, stream=None):
+    """The stream handle of a call on these tensors (None entries aside), which
+    must all be on the current device, as must a stream that is given: a kernel
+    launched elsewhere would fault on their addresses."""
+    torch = _torch()
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
+
+
+def _opt(t, dtypes, name):
+    return None if t is None else _ptr(t, dtypes, name)
+
+
+def _i32():
+    return (_torch().int32,)
+
+
+def _bf():
+    return (_torch().bfloat16,)
+
+
+def _check_plan(plan, M, L):
+    _need(plan.numel() == L + 2 + M, f"plan: {plan.numel()} elements, expected {L + 2 + M} for {M} rows and {L} adapters")
+
+
+def lora_plan(ids, n_adapters, plan=None, stream=None):
+    """plan (int32 [n_adapters + 2 + M]) = the rows of ids (int32 [M]) ordered by adapter: group
+    starts, then rows (see bsgemm.h); an id outside [0, n_adapters) means no adapter."""
+    torch = _torch()
+    _need(ids.dim() == 1, f"ids must be 1-D, got shape {tuple(ids.shape)}")
+    _need(n_adapters >= 1, f"lora_plan: n_adapters must be at least 1, got {n_adapters}")
+    M = ids.shape[0]
+    if plan is None:
+        plan = torch.empty(n_adapters + 2 + M, dtype=torch.int32, device=ids.device)
+    _check_plan(plan, M, n_adapters)
+    pi, pp = _ptr(ids, _i32(), "ids"), _ptr(plan, _i32(), "plan")
+    st = load().lora_plan(pi, pp, M, n_adapters, _here("lora_plan", ids, plan, stream=stream))
+    _check(st, "lora_plan")
+    return plan
+
+
+def lora_shrink(x, A, plan, H=None, stream=None):
+    """H (fp32 [M,R]) = each row of x (bf16 [M,K]) times its adapter's A (bf16 [n_adapters,R,K])
+    transposed, by the plan of lora_plan; zero rows where there is no adapter."""
+    torch = _torch()
+    M, K = _dims2(x, "x")
+    _need(A.dim() == 3 and A.shape[2] == K, f"A: shape {tuple(A.shape)}, expected [n_adapters, R, {K}]")
+    L, R = A.shape[0], A.shape[1]
+    _check_plan(plan, M, L)
+    if H is None:
+        H = torch.empty((M, R), dtype=torch.float32, device=x.device)
+    _room(H, M * R, "H")
+    ptrs = (_ptr(x, _bf(), "x"), _ptr(A, _bf(), "A"), _ptr(plan, _i32(), "plan"), _ptr(H, _f32(), "H"))
+    if M == 0:
+        return H
+    st = load().lora_shrink(*ptrs, M, K, L, R, _here("lora_shrink", x, A, plan, H, stream=stream))
+    _check(st, "lora_shrink")
+    return H
+
+
+def _check_lora(H, B, scale, N, what):
+    M, R = _dims2(H, "H")
+    _need(B.dim() == 3 and B.shape[2] == R, f"{what}: shape {tuple(B.shape)}, expected [n_adapters, N, {R}]")
+    if N is not None:
+        _need(B.shape[1] == N, f"{what}: shape {tuple(B.shape)}, expected [n_adapters, {N}, {R}]")
+    if scale is not None:
+        _shape(scale, (B.shape[0],), "scale")
+    return M, B.shape[1], B.shape[0], R
+
+
+def lora_expand(H, B, plan, base, out=None, scale=None, bands=1, band_stride=0, stream=None):
+    """out (bf16 bands) = base + scale[a] * (H [M,R] fp32 x B[a]^T), B bf16 [n_adapters,N,R], a each
+    row's adapter by the plan; base and out are banded as bsgemm_fp8's C; out=base works in place."""
+    torch = _torch()
+    M, N, L, R = _check_lora(H, B, scale, None, "B")
+    _check_plan(plan, M, L)
+    need = _band_elems(M, N, bands, band_stride)
+    _need(base.numel() >= need, f"base: {base.numel()} elements, the call reads {need}")
+    if out is None:
+        out = torch.empty(need, dtype=torch.bfloat16, device=base.device)
+    _room(out, need, "out")
+    ptrs = (_ptr(H, _f32(), "H"), _ptr(B, _bf(), "B"), _opt(scale, _f32(), "scale"), _ptr(plan, _i32(), "plan"),
+            _ptr(base, _bf(), "base"), _ptr(out, _bf(), "out"))
+    if M == 0:
+        return out
+    st = load().lora_expand(*ptrs, M, N, L, R, bands, band_stride,
+                            _here("lora_expand", H, B, scale, plan, base, out, stream=stream))
+    _check(st, "lora_expand")
+    return out
+
+
+def bsgemm_fp8_lora(A, a_scale, B, b_scale, H, lora_B, ids, scale=None, C=None, bands=1, band_stride=0,
+                    stream=None):
+    """bsgemm_fp8 plus scale[a] * (H [M,R] fp32 x lora_B[a]^T) for each row's adapter a = ids[row]
+    (lora_B bf16 [n_adapters,N,R]), added in fp32 before the rounding to bf16."""
+    torch = _torch()
+    M, N, K = _check_gemm_operands(A, a_scale, B, b_scale, 128, "bsgemm_fp8_lora")
+    Mh, _, L, R = _check_lora(H, lora_B, scale, N, "lora_B")
+    _need(Mh == M, f"H: {Mh} rows, A has {M}")
+    _shape(ids, (M,), "ids")
+    need = _band_elems(M, N, bands, band_stride)
+    if C is None:
+        C = torch.empty(need, dtype=torch.bfloat16, device=A.device)
+    _room(C, need, "C")
+    ptrs = (_ptr(A, _u8(), "A"), _ptr(a_scale, _f32(), "a_scale"), _ptr(B, _u8(), "B"),
+            _ptr(b_scale, _f32(), "b_scale"), _ptr(H, _f32(), "H"), _ptr(lora_B, _bf(), "lora_B"),
+            _opt(scale, _f32(), "scale"), _ptr(ids, _i32(), "ids"), _ptr(C, _b16(), "C"))
+    if M == 0:
+        return C
+    st = load().bsgemm_fp8_lora(*ptrs, M, N, K, L, R, bands, band_stride,
+                                _here("bsgemm_fp8_lora", A, a_scale, B, b_scale, H, lora_B, scale, ids, C,
+                                      stream=stream))
+    _check(st, "bsgemm_fp8_lora")
+    return C
+
+
+def resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.0, beta=1.0, eps=1e-6, quant=0,
+            resid_out=None, z=None, q=None, q_scale=None, stream=None):
+    """(resid_out, z, q, q_scale): h = alpha * resid + beta * gate * norm(y; post_w) as the new residual,
+    z = norm(h; pre_w) in bf16, and z's e4m3 codes with 1x128 fp32 (quant=128) or 1x32 E8M0
+    (quant=32) scales, in one pass.
+
+    y: bf16 [rows,N], or e4m3 codes with y_scale fp32 [rows] (the fp8 wire).  resid: bf16 or fp32
+    [rows,N]; resid_out=resid updates it in place.  post_w, pre_w: bf16 [N] or None (no norm
+    after the block; unit weight).  gate: bf16 [N] or [rows,N] or None.  z is written if a
+    buffer is given, or (quant=0) always; what is not written is returned as None."""
+    torch = _torch()
+    rows, N = _dims2(y, "y")
+    _shape(resid, (rows, N), "resid")
+    _need(quant in (0, 32, 128), f"resnorm: quant must be 0, 32 or 128, got {quant}")
+    _need(quant == 0 or N % quant == 0, f"resnorm: N={N} is not a multiple of quant={quant}")
+    if y_scale is not None:
+        _need(y_scale.numel() == rows, f"y_scale: {y_scale.numel()} elements for {rows} rows")
+    if post_w is not None:
+        _shape(post_w, (N,), "post_w")
+    if pre_w is not None:
+        _shape(pre_w, (N,), "pre_w")
+    gate_row = 0
+    if gate is not None and gate.dim() != 1:
+        _shape(gate, (rows, N), "gate")
+        gate_row = N
+    elif gate is not None:
+        _shape(gate, (N,), "gate")
+    if resid_out is None:
+        resid_out = torch.empty_like(resid)
+    _need(resid_out.dtype == resid.dtype, f"resid_out is {resid_out.dtype}, resid is {resid.dtype}")
+    _room(resid_out, rows * N, "resid_out")
+    if quant:
+        if q is None:
+            q = torch.empty((rows, N), dtype=torch.uint8, device=y.device)
+        if q_scale is None:
+            q_scale = torch.empty((rows, N // quant), dtype=torch.float32 if quant == 128 else torch.uint8,
+                                  device=y.device)
+        _room(q, rows * N, "q")
+        _room(q_scale, rows * (N // quant), "q_scale")
+    else:
+        _need(q is None and q_scale is None, "resnorm: q and q_scale need quant=32 or 128")
+        if z is None:
+            z = torch.empty((rows, N), dtype=torch.bfloat16, device=y.device)
+    if z is not None:
+        _room(z, rows * N, "z")
+    rt = (torch.bfloat16, torch.float32)
+    py = _ptr(y, _u8() if y_scale is not None else _bf(), "y")
+    ptrs = (py, _opt(y_scale, _f32(), "y_scale"), _ptr(resid, rt, "resid"), _opt(post_w, _bf(), "post_w"),
+            _opt(gate, _bf(), "gate"), gate_row, _opt(pre_w, _bf(), "pre_w"), _ptr(resid_out, rt, "resid_out"),
+            _opt(z, _bf(), "z"), _opt(q, _u8(), "q"),
+            _opt(q_scale, _f32() if quant == 128 else (torch.uint8,), "q_scale"))
+    if rows == 0:
+        return resid_out, z, q, q_scale
+    st = load().resnorm(*ptrs, rows, N, int(resid.dtype == torch.float32), quant, alpha, beta, eps,
+                        _here("resnorm", y, y_scale, resid, post_w, gate, pre_w, resid_out, z, q, q_scale,
+                              stream=stream))
+    _check(st, "resnorm")
+    return resid_out, z, q, q_scale

@@ -61,6 +61,7 @@
 
 #include "codec.hpp"
 #include "launch.hpp"
+#include "lora.hpp"
 
 namespace {
 
@@ -72,7 +73,6 @@ constexpr int GROUP_M = 4;
 constexpr int NUM_XCD = 8;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -860,12 +860,74 @@ __device__ __forceinline__ void store_tile(const v4f (&acc)[TM][TN], const GemmA
     }
 }
 
+// ---- adapters --------------------------------------------------------------
+struct LoraGemmArgs {
+    LoraArgs lora;
+    const int32_t *ids;     // int32 [M]: a row's adapter; outside [0, L): none
+};
+
+// Adds scale[a] (H[m] B[a]^T), a = ids[m], to the finished accumulators of a
+// wave's 128 x 64 sub-tile, in fp32, before the one rounding to bf16.  A wave
+// goes through the distinct adapters of its 128 rows (one or two in a prefill
+// chunk, whose requests are runs of rows).  For each it loads the adapter's 64
+// columns of B once per 32 of R, in the sub-tiles' own column order, and gives
+// every 16-row group that has such a row its products, with H zero in the rows
+// of other adapters.  A group without one is skipped, so a row of no adapter
+// keeps its product bit for bit unless it shares a group with others', where
+// it gets a zero added, which changes nothing but the sign of a zero.
+__device__ __forceinline__ void lora_add(v4f (&acc)[TM][TN], const GemmArgs &g, const LoraGemmArgs &q, int64_t m0,
+                                         int64_t n0, int wm, int wn, int lane) {
+    const int frow = lane & 15, fg = lane >> 4;
+    const int64_t mw = m0 + wm * WM;
+    int id[2];
+    uint64_t todo[2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const int64_t m = mw + 64 * h + lane;
+        id[h] = -1;
+        if (m < g.M) {
+            const int a = q.ids[m];
+            if ((uint32_t)a < (uint32_t)q.lora.L) id[h] = a;
+        }
+        todo[h] = __ballot(id[h] >= 0);
+    }
+    while (todo[0] | todo[1]) {
+        const int a = todo[0] ? __builtin_amdgcn_readlane(id[0], __ffsll((unsigned long long)todo[0]) - 1)
+                              : __builtin_amdgcn_readlane(id[1], __ffsll((unsigned long long)todo[1]) - 1);
+        const uint64_t mine[2] = {__ballot(id[0] == a), __ballot(id[1] == a)};
+        todo[0] &= ~mine[0];
+        todo[1] &= ~mine[1];
+        const float s = q.lora.scale ? q.lora.scale[a] : 1.0f;
+        const uint16_t *br[TN];
+#pragma unroll
+        for (int j = 0; j < TN; j++) br[j] = lora_brow(q.lora, a, n0 + wn * WN + lora_col(j, frow), g.N);
+        for (int r0 = 0; r0 < q.lora.R; r0 += 32) {
+            const int r = r0 + 8 * fg;
+            v8bf b[TN];
+#pragma unroll
+            for (int j = 0; j < TN; j++) b[j] = lora_load_b(br[j], r, q.lora.R);
+#pragma unroll
+            for (int i = 0; i < TM; i++) {
+                const uint32_t rows = (uint32_t)(mine[i >> 2] >> (16 * (i & 3))) & 0xFFFFu;
+                if (!rows) continue;
+                v8bf hi, lo;
+                lora_load_h(q.lora, mw + 16 * i + frow, (rows >> frow) & 1, r, s, hi, lo);
+#pragma unroll
+                for (int j = 0; j < TN; j++) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], hi, acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], lo, acc[i][j], 0, 0, 0);
+                }
+            }
+        }
+    }
+}
+
 // One 256x256 output tile.  MODE_BS: blockscale operands, A and B staged in
 // LDS; MODE_PB: blockscale with the prepacked B loaded into registers;
 // MODE_MX: mxfp8 operands (E8M0 scales per 1x32 block, applied by the scaled
 // MFMA).
-template <int MODE>
-__device__ __forceinline__ void gemm_tile(const GemmArgs &g) {
+template <int MODE, bool LORA = false>
+__device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs &q = {}) {
     int64_t m0, n0;
     if (!tile_of(g, blockIdx.x, m0, n0)) return;
 
@@ -975,6 +1037,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g) {
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the last (empty) DMA is retired
 
+    if constexpr (LORA) lora_add(acc, g, q, m0, n0, wm, wn, lane);
     store_tile<MODE>(acc, g, m0, n0, wave, lane);
 }
 
@@ -1282,6 +1345,10 @@ __global__ void __launch_bounds__(NTHREADS) mxgemm_persistent_kernel(GemmArgs g)
 
 __global__ void __launch_bounds__(NTHREADS) bsgemm_tile_kernel(GemmArgs g) { gemm_tile<MODE_BS>(g); }
 
+__global__ void __launch_bounds__(NTHREADS) bsgemm_lora_tile_kernel(GemmArgs g, LoraGemmArgs q) {
+    gemm_tile<MODE_BS, true>(g, q);
+}
+
 __global__ void __launch_bounds__(NTHREADS) bsgemm_pb_tile_kernel(GemmArgs g) { gemm_tile<MODE_PB>(g); }
 
 __global__ void __launch_bounds__(NTHREADS) mxgemm_tile_kernel(GemmArgs g) { gemm_tile<MODE_MX>(g); }
@@ -1365,6 +1432,14 @@ int bs_launch_gemm(const uint8_t *A, const float *sa, const uint8_t *B, const fl
         return bs_enqueue(bsgemm_persistent_kernel, dim3(persistent_grid(g, stream)), dim3(NTHREADS),
                           stream, g);
     return bs_enqueue(bsgemm_tile_kernel, dim3(gemm_grid(g)), dim3(NTHREADS), stream, g);
+}
+
+int bs_launch_gemm_lora(const uint8_t *A, const float *sa, const uint8_t *B, const float *sb, uint16_t *C,
+                        const LoraArgs &lora, const int32_t *ids, int64_t M, int64_t N, int64_t K, int64_t band_rows,
+                        int64_t band_stride, hipStream_t stream) {
+    const GemmArgs g = gemm_args(A, sa, B, sb, C, M, N, K, band_rows, band_stride);
+    const LoraGemmArgs q = {lora, ids};
+    return bs_enqueue(bsgemm_lora_tile_kernel, dim3(gemm_grid(g)), dim3(NTHREADS), stream, g, q);
 }
 
 int bs_launch_gemm_pb(const uint8_t *A, const float *sa, const uint8_t *Bp, const float *sb,

@@ -21,6 +21,18 @@
  *                per 1x32 block on both A and B, applied by the MFMA
  *   mxq_e4m3     bf16 -> e4m3 codes + E8M0 1x32 scales (mxgemm_fp8's operands)
  *
+ * and what stands around that layer in a serving stack:
+ *
+ *   lora_plan    orders a batch's rows by the low-rank adapter each one uses
+ *   lora_shrink  H[m] = x[m] A[a]^T, the first low-rank product of every row
+ *   lora_expand  out[m] = base[m] + scale[a] (H[m] B[a]^T), the second one added
+ *                to a finished row-banded output
+ *   bsgemm_fp8_lora  bsgemm_fp8 with the second product added to its fp32
+ *                accumulators, so C is written once
+ *   resnorm      norm after a block, gate, scaled residual, norm before the
+ *                next block and its e4m3 operand, in one pass; takes the
+ *                gathered fp8 wire or a bf16 output
+ *
  * Pages defining the operations (cited by title and section):
  *   [PR40757] sglang PR 40757 "[AMD][gfx950] DSV4: fuse wo_b's GEMM with its
  *             all-reduce via mori cco": "What" (block-scale fp8 GEMM followed
@@ -312,6 +324,136 @@ bs_status mxq_e4m3(const uint16_t *x, uint8_t *q, uint8_t *scale,
  */
 bs_status band_rowq_e4m3(const uint16_t *const *parts, int32_t P, uint8_t *q,
                          float *scale, int64_t rows, int64_t N, void *stream);
+
+/*
+ * Row order of a batch whose rows use different low-rank adapters.  ids[m] is
+ * row m's adapter, in [0, n_adapters); any other value means that the row has
+ * none.  With key(m) = ids[m], or n_adapters for a row without an adapter:
+ *
+ *   plan[a]  for a = 0 .. n_adapters + 1: the number of rows with key < a
+ *            (so plan[n_adapters] rows have an adapter, and
+ *            plan[n_adapters + 1] = M)
+ *   plan[n_adapters + 2 + i], i = 0 .. M - 1: the rows ordered by key, rows of
+ *            one key in ascending order
+ *
+ * One plan serves every layer that the batch passes through.
+ *
+ *   ids   int32 [M] (may be null when M = 0)
+ *   plan  int32 [n_adapters + 2 + M]
+ *
+ * Requirements: 0 <= M < 2^30; 1 <= n_adapters <= 4096; 4-byte alignment; plan
+ * must not overlap ids.  M = 0 writes n_adapters + 2 zeros.
+ */
+bs_status lora_plan(const int32_t *ids, int32_t *plan, int64_t M, int64_t n_adapters, void *stream);
+
+/*
+ * First low-rank product: H[m, r] = sum_k x[m, k] * A[a, r, k], a = row m's
+ * adapter by the plan; H[m] = 0 for a row without one.  bf16 products summed
+ * in fp32, and not rounded further: H is fp32.  Under row parallelism x and A
+ * hold this GPU's part of K, and H is its partial sum: lora_expand and
+ * bsgemm_fp8_lora add it to the same GPU's partial output, whose reduction then
+ * completes both.
+ *
+ *   x     bf16 [M, K] (finite)
+ *   A     bf16 [n_adapters, R, K] (finite; an adapter of a smaller rank has
+ *         zero rows)
+ *   plan  as lora_plan writes it for these rows and n_adapters.  Entries that
+ *         lie outside the batch are ignored, but no check finds that a plan
+ *         belongs to another batch
+ *   H     fp32 [M, R]
+ *
+ * Requirements: 0 <= M < 2^30; K > 0, K % 8 == 0, K <= 2^22; 1 <= n_adapters
+ * <= 4096; R % 8 == 0, 8 <= R <= 256; x, A, H 16-byte aligned, plan 4-byte; H
+ * must not overlap an input.
+ */
+bs_status lora_shrink(const uint16_t *x, const uint16_t *A, const int32_t *plan, float *H, int64_t M,
+                      int64_t K, int64_t n_adapters, int64_t R, void *stream);
+
+/*
+ * Second low-rank product, added to a finished output:
+ *
+ *   out[m, n] = bf16_rne( base[m, n] + scale[a] * sum_r H[m, r] * B[a, n, r] )
+ *
+ * for a row with adapter a; out[m] = base[m] for one without.  The sum is fp32;
+ * scale * H enters the products as two bf16 (17 bits of significand).  base and
+ * out are row-banded as bsgemm_fp8's C (bands, band_stride as there); elements
+ * between bands are untouched.  out may be base itself.
+ *
+ *   H      fp32 [M, R] (finite; the rows without an adapter are not read)
+ *   B      bf16 [n_adapters, N, R] (finite)
+ *   scale  fp32 [n_adapters] or null (1)
+ *   plan   as for lora_shrink
+ *   base   bf16 bands;  out  bf16 bands
+ *
+ * Requirements: as lora_shrink for M, n_adapters and R; N > 0, N % 8 == 0;
+ * 1 <= bands <= 64 and M % bands == 0; band_stride 0 or >= (M / bands) * N and
+ * a multiple of 8; H, B, base, out 16-byte aligned, scale and plan 4-byte; out
+ * equals base or does not overlap it, and overlaps no other input.
+ */
+bs_status lora_expand(const float *H, const uint16_t *B, const float *scale, const int32_t *plan,
+                      const uint16_t *base, uint16_t *out, int64_t M, int64_t N, int64_t n_adapters,
+                      int64_t R, int32_t bands, int64_t band_stride, void *stream);
+
+/*
+ * bsgemm_fp8 with its rows' adapters: to the finished fp32 accumulator of row m
+ * is added scale[a] * sum_r H[m, r] * lora_B[a, n, r], a = ids[m], before the one
+ * rounding to bf16.  A row whose id is outside [0, n_adapters) gets bsgemm_fp8's
+ * result, bit for bit (the sign of a zero apart), and its H is not read.  This
+ * reads ids directly and needs no plan: prefer it to bsgemm_fp8 followed by
+ * lora_expand, which writes and reads C once more; its cost grows with the
+ * number of different adapters among 128 consecutive rows.
+ *
+ *   A, a_scale, B, b_scale, C, bands, band_stride  as for bsgemm_fp8
+ *   H           fp32 [M, R] (finite), from lora_shrink
+ *   lora_B      bf16 [n_adapters, N, R] (finite)
+ *   lora_scale  fp32 [n_adapters] or null (1)
+ *   ids         int32 [M]
+ *
+ * Requirements: those of bsgemm_fp8, and of lora_expand for M, n_adapters, R and
+ * the alignments; C must not overlap an input.
+ */
+bs_status bsgemm_fp8_lora(const uint8_t *A, const float *a_scale, const uint8_t *B,
+                          const float *b_scale, const float *H, const uint16_t *lora_B,
+                          const float *lora_scale, const int32_t *ids, uint16_t *C, int64_t M, int64_t N,
+                          int64_t K, int64_t n_adapters, int64_t R, int32_t bands, int64_t band_stride,
+                          void *stream);
+
+/*
+ * The step between two blocks, row by row, with rms(v) = sqrt(mean(v^2) + eps):
+ *
+ *   y = decode(y) * y_scale[row]        if y_scale is given (the fp8 wire, as
+ *                                       rowdq_e4m3 but not rounded to bf16)
+ *   p = y / rms(y) * post_w             if post_w is given, else p = y
+ *   h = alpha * resid + beta * gate * p      (gate = 1 if null)
+ *   resid_out = h, rounded to the residual's type
+ *   z = h / rms(h) * pre_w              (pre_w = 1 if null)
+ *   q = e4m3(z / s) with s in q_scale   if q_block is 128 (fp32 scale per 1x128
+ *                                       block, s = amax / 448) or 32 (E8M0 scale
+ *                                       per 1x32 block, as mxq_e4m3)
+ *
+ * All of it in fp32, each output rounded once: z and q come from the unrounded
+ * h, and q from the unrounded z.  An all-zero scale block gets scale 0 (byte 0)
+ * and codes 0x00.
+ *
+ *   y          bf16 [rows, N], or e4m3 [rows, N] with y_scale fp32 [rows]
+ *   resid      bf16 [rows, N], or fp32 if resid_f32 is 1; resid_out the same
+ *              type, and may be resid itself
+ *   post_w, pre_w  bf16 [N] or null
+ *   gate       bf16 [N] if gate_row is 0, [rows, N] if gate_row is N; or null
+ *   z          bf16 [rows, N] or null
+ *   q, q_scale e4m3 [rows, N] with fp32 [rows, N/128] or bytes [rows, N/32];
+ *              both null if q_block is 0
+ *   (finite values whose squares sum within fp32's range)
+ *
+ * Requirements: 0 <= rows < 2^31; N > 0, N % 8 == 0 (N % q_block == 0 with
+ * q), N <= 16384; eps > 0 and alpha, beta, eps finite; every pointer 16-byte
+ * aligned but y_scale and q_scale (4-byte; E8M0 bytes any); outputs overlap
+ * neither each other nor an input, except resid_out == resid.
+ */
+bs_status resnorm(const void *y, const float *y_scale, const void *resid, const uint16_t *post_w,
+                  const uint16_t *gate, int64_t gate_row, const uint16_t *pre_w, void *resid_out,
+                  uint16_t *z, uint8_t *q, void *q_scale, int64_t rows, int64_t N, int32_t resid_f32,
+                  int32_t q_block, float alpha, float beta, float eps, void *stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char *bs_status_str(bs_status status);
