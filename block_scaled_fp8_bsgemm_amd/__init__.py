@@ -366,72 +366,102 @@ def band_rowq_e4m3(parts, q=None, scale=None, stream=None):
     return q, scale
 
 
-def _here(name, *tensors, stream=None):
-    """The stream handle of a call on these tensors (None entries aside), which
-    must all be on the current device, as must a stream that is given: a kernel
-    launched elsewhere would fault on their addresses."""
-    torch = _torch()
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+class _Types:
+    """The dtypes the calls below take, formed once: such a call costs a few
+    microseconds on the host, and a decode step makes many."""
+
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.u8, self.bytes, self.b16, self.f32 = _u8(), (torch.uint8,), _b16(), _f32()
+        self.i32, self.bf, self.resid = (torch.int32,), (torch.bfloat16,), (torch.bfloat16, torch.float32)
+
+
+_types = None
+
+
+def _ty():
+    global _types
+    if _types is None:
+        _types = _Types()
+    return _types
+
+
+def _args(what, stream, *args):
+    """The pointers of a call's (tensor or None, dtypes, name) arguments, and its
+    stream's handle.  The tensors must be on one device, which must be the current
+    one, as must a stream that is given: a kernel launched elsewhere would fault
+    on their addresses."""
+    torch = _ty().torch
+    out, dev = [], None
+    for t, dtypes, name in args:
+        if t is None:
+            out.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{name} must be a device tensor")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{what}: tensors on cuda:{dev} and cuda:{d}")
+        out.append(t.data_ptr())
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{what}: tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {dev}")
-    return stream.cuda_stream
-
-
-def _opt(t, dtypes, name):
-    return None if t is None else _ptr(t, dtypes, name)
-
-
-def _i32():
-    return (_torch().int32,)
-
-
-def _bf():
-    return (_torch().bfloat16,)
+        handle = torch._C._cuda_getCurrentRawStream(dev)   # current_stream() alone takes 2.7 us
+    elif stream.device.index != dev:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+    else:
+        handle = stream.cuda_stream
+    return out, handle
 
 
 def _check_plan(plan, M, L):
-    _need(plan.numel() == L + 2 + M, f"plan: {plan.numel()} elements, expected {L + 2 + M} for {M} rows and {L} adapters")
+    if plan.numel() != L + 2 + M:
+        raise ValueError(f"plan: {plan.numel()} elements, expected {L + 2 + M} for {M} rows and {L} adapters")
+
+
+def _is(t, shape, name):
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def lora_plan(ids, n_adapters, plan=None, stream=None):
     """plan (int32 [n_adapters + 2 + M]) = the rows of ids (int32 [M]) ordered by adapter: group
     starts, then rows (see bsgemm.h); an id outside [0, n_adapters) means no adapter."""
-    torch = _torch()
+    ty = _ty()
     _need(ids.dim() == 1, f"ids must be 1-D, got shape {tuple(ids.shape)}")
     _need(n_adapters >= 1, f"lora_plan: n_adapters must be at least 1, got {n_adapters}")
     M = ids.shape[0]
     if plan is None:
-        plan = torch.empty(n_adapters + 2 + M, dtype=torch.int32, device=ids.device)
+        plan = ty.torch.empty(n_adapters + 2 + M, dtype=ty.torch.int32, device=ids.device)
     _check_plan(plan, M, n_adapters)
-    pi, pp = _ptr(ids, _i32(), "ids"), _ptr(plan, _i32(), "plan")
-    st = load().lora_plan(pi, pp, M, n_adapters, _here("lora_plan", ids, plan, stream=stream))
-    _check(st, "lora_plan")
+    p, st = _args("lora_plan", stream, (ids, ty.i32, "ids"), (plan, ty.i32, "plan"))
+    _check(load().lora_plan(*p, M, n_adapters, st), "lora_plan")
     return plan
 
 
 def lora_shrink(x, A, plan, H=None, stream=None):
     """H (fp32 [M,R]) = each row of x (bf16 [M,K]) times its adapter's A (bf16 [n_adapters,R,K])
     transposed, by the plan of lora_plan; zero rows where there is no adapter."""
-    torch = _torch()
+    ty = _ty()
     M, K = _dims2(x, "x")
     _need(A.dim() == 3 and A.shape[2] == K, f"A: shape {tuple(A.shape)}, expected [n_adapters, R, {K}]")
-    L, R = A.shape[0], A.shape[1]
+    L, R, _ = A.shape
     _check_plan(plan, M, L)
     if H is None:
-        H = torch.empty((M, R), dtype=torch.float32, device=x.device)
+        H = ty.torch.empty((M, R), dtype=ty.torch.float32, device=x.device)
     _room(H, M * R, "H")
-    ptrs = (_ptr(x, _bf(), "x"), _ptr(A, _bf(), "A"), _ptr(plan, _i32(), "plan"), _ptr(H, _f32(), "H"))
-    if M == 0:
-        return H
-    st = load().lora_shrink(*ptrs, M, K, L, R, _here("lora_shrink", x, A, plan, H, stream=stream))
-    _check(st, "lora_shrink")
+    p, st = _args("lora_shrink", stream, (x, ty.bf, "x"), (A, ty.bf, "A"), (plan, ty.i32, "plan"), (H, ty.f32, "H"))
+    if M:
+        _check(load().lora_shrink(*p, M, K, L, R, st), "lora_shrink")
     return H
 
 
@@ -441,28 +471,25 @@ def _check_lora(H, B, scale, N, what):
     if N is not None:
         _need(B.shape[1] == N, f"{what}: shape {tuple(B.shape)}, expected [n_adapters, {N}, {R}]")
     if scale is not None:
-        _shape(scale, (B.shape[0],), "scale")
+        _is(scale, (B.shape[0],), "scale")
     return M, B.shape[1], B.shape[0], R
 
 
 def lora_expand(H, B, plan, base, out=None, scale=None, bands=1, band_stride=0, stream=None):
     """out (bf16 bands) = base + scale[a] * (H [M,R] fp32 x B[a]^T), B bf16 [n_adapters,N,R], a each
     row's adapter by the plan; base and out are banded as bsgemm_fp8's C; out=base works in place."""
-    torch = _torch()
+    ty = _ty()
     M, N, L, R = _check_lora(H, B, scale, None, "B")
     _check_plan(plan, M, L)
     need = _band_elems(M, N, bands, band_stride)
     _need(base.numel() >= need, f"base: {base.numel()} elements, the call reads {need}")
     if out is None:
-        out = torch.empty(need, dtype=torch.bfloat16, device=base.device)
+        out = ty.torch.empty(need, dtype=ty.torch.bfloat16, device=base.device)
     _room(out, need, "out")
-    ptrs = (_ptr(H, _f32(), "H"), _ptr(B, _bf(), "B"), _opt(scale, _f32(), "scale"), _ptr(plan, _i32(), "plan"),
-            _ptr(base, _bf(), "base"), _ptr(out, _bf(), "out"))
-    if M == 0:
-        return out
-    st = load().lora_expand(*ptrs, M, N, L, R, bands, band_stride,
-                            _here("lora_expand", H, B, scale, plan, base, out, stream=stream))
-    _check(st, "lora_expand")
+    p, st = _args("lora_expand", stream, (H, ty.f32, "H"), (B, ty.bf, "B"), (scale, ty.f32, "scale"),
+                  (plan, ty.i32, "plan"), (base, ty.bf, "base"), (out, ty.bf, "out"))
+    if M:
+        _check(load().lora_expand(*p, M, N, L, R, bands, band_stride, st), "lora_expand")
     return out
 
 
@@ -470,24 +497,20 @@ def bsgemm_fp8_lora(A, a_scale, B, b_scale, H, lora_B, ids, scale=None, C=None, 
                     stream=None):
     """bsgemm_fp8 plus scale[a] * (H [M,R] fp32 x lora_B[a]^T) for each row's adapter a = ids[row]
     (lora_B bf16 [n_adapters,N,R]), added in fp32 before the rounding to bf16."""
-    torch = _torch()
+    ty = _ty()
     M, N, K = _check_gemm_operands(A, a_scale, B, b_scale, 128, "bsgemm_fp8_lora")
     Mh, _, L, R = _check_lora(H, lora_B, scale, N, "lora_B")
     _need(Mh == M, f"H: {Mh} rows, A has {M}")
-    _shape(ids, (M,), "ids")
+    _is(ids, (M,), "ids")
     need = _band_elems(M, N, bands, band_stride)
     if C is None:
-        C = torch.empty(need, dtype=torch.bfloat16, device=A.device)
+        C = ty.torch.empty(need, dtype=ty.torch.bfloat16, device=A.device)
     _room(C, need, "C")
-    ptrs = (_ptr(A, _u8(), "A"), _ptr(a_scale, _f32(), "a_scale"), _ptr(B, _u8(), "B"),
-            _ptr(b_scale, _f32(), "b_scale"), _ptr(H, _f32(), "H"), _ptr(lora_B, _bf(), "lora_B"),
-            _opt(scale, _f32(), "scale"), _ptr(ids, _i32(), "ids"), _ptr(C, _b16(), "C"))
-    if M == 0:
-        return C
-    st = load().bsgemm_fp8_lora(*ptrs, M, N, K, L, R, bands, band_stride,
-                                _here("bsgemm_fp8_lora", A, a_scale, B, b_scale, H, lora_B, scale, ids, C,
-                                      stream=stream))
-    _check(st, "bsgemm_fp8_lora")
+    p, st = _args("bsgemm_fp8_lora", stream, (A, ty.u8, "A"), (a_scale, ty.f32, "a_scale"), (B, ty.u8, "B"),
+                  (b_scale, ty.f32, "b_scale"), (H, ty.f32, "H"), (lora_B, ty.bf, "lora_B"), (scale, ty.f32, "scale"),
+                  (ids, ty.i32, "ids"), (C, ty.b16, "C"))
+    if M:
+        _check(load().bsgemm_fp8_lora(*p, M, N, K, L, R, bands, band_stride, st), "bsgemm_fp8_lora")
     return C
 
 
@@ -501,28 +524,28 @@ def resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.
     [rows,N]; resid_out=resid updates it in place.  post_w, pre_w: bf16 [N] or None (no norm
     after the block; unit weight).  gate: bf16 [N] or [rows,N] or None.  z is written if a
     buffer is given, or (quant=0) always; what is not written is returned as None."""
-    torch = _torch()
+    ty = _ty()
+    torch = ty.torch
     rows, N = _dims2(y, "y")
-    _shape(resid, (rows, N), "resid")
+    _is(resid, (rows, N), "resid")
     _need(quant in (0, 32, 128), f"resnorm: quant must be 0, 32 or 128, got {quant}")
-    _need(quant == 0 or N % quant == 0, f"resnorm: N={N} is not a multiple of quant={quant}")
-    if y_scale is not None:
-        _need(y_scale.numel() == rows, f"y_scale: {y_scale.numel()} elements for {rows} rows")
+    if y_scale is not None and y_scale.numel() != rows:
+        raise ValueError(f"y_scale: {y_scale.numel()} elements for {rows} rows")
     if post_w is not None:
-        _shape(post_w, (N,), "post_w")
+        _is(post_w, (N,), "post_w")
     if pre_w is not None:
-        _shape(pre_w, (N,), "pre_w")
+        _is(pre_w, (N,), "pre_w")
     gate_row = 0
-    if gate is not None and gate.dim() != 1:
-        _shape(gate, (rows, N), "gate")
-        gate_row = N
-    elif gate is not None:
-        _shape(gate, (N,), "gate")
+    if gate is not None:
+        gate_row = N if gate.dim() == 2 else 0
+        _is(gate, (rows, N) if gate_row else (N,), "gate")
     if resid_out is None:
         resid_out = torch.empty_like(resid)
-    _need(resid_out.dtype == resid.dtype, f"resid_out is {resid_out.dtype}, resid is {resid.dtype}")
+    elif resid_out.dtype != resid.dtype:
+        raise ValueError(f"resid_out is {resid_out.dtype}, resid is {resid.dtype}")
     _room(resid_out, rows * N, "resid_out")
     if quant:
+        _need(N % quant == 0, f"resnorm: N={N} is not a multiple of quant={quant}")
         if q is None:
             q = torch.empty((rows, N), dtype=torch.uint8, device=y.device)
         if q_scale is None:
@@ -536,16 +559,11 @@ def resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.
             z = torch.empty((rows, N), dtype=torch.bfloat16, device=y.device)
     if z is not None:
         _room(z, rows * N, "z")
-    rt = (torch.bfloat16, torch.float32)
-    py = _ptr(y, _u8() if y_scale is not None else _bf(), "y")
-    ptrs = (py, _opt(y_scale, _f32(), "y_scale"), _ptr(resid, rt, "resid"), _opt(post_w, _bf(), "post_w"),
-            _opt(gate, _bf(), "gate"), gate_row, _opt(pre_w, _bf(), "pre_w"), _ptr(resid_out, rt, "resid_out"),
-            _opt(z, _bf(), "z"), _opt(q, _u8(), "q"),
-            _opt(q_scale, _f32() if quant == 128 else (torch.uint8,), "q_scale"))
-    if rows == 0:
-        return resid_out, z, q, q_scale
-    st = load().resnorm(*ptrs, rows, N, int(resid.dtype == torch.float32), quant, alpha, beta, eps,
-                        _here("resnorm", y, y_scale, resid, post_w, gate, pre_w, resid_out, z, q, q_scale,
-                              stream=stream))
-    _check(st, "resnorm")
+    p, st = _args("resnorm", stream, (y, ty.bf if y_scale is None else ty.u8, "y"), (y_scale, ty.f32, "y_scale"),
+                  (resid, ty.resid, "resid"), (post_w, ty.bf, "post_w"), (gate, ty.bf, "gate"), (pre_w, ty.bf, "pre_w"),
+                  (resid_out, ty.resid, "resid_out"), (z, ty.bf, "z"), (q, ty.u8, "q"),
+                  (q_scale, ty.f32 if quant == 128 else ty.bytes, "q_scale"))
+    if rows:
+        _check(load().resnorm(*p[:5], gate_row, *p[5:], rows, N, int(resid.dtype is torch.float32), quant, alpha, beta,
+                              eps, st), "resnorm")
     return resid_out, z, q, q_scale

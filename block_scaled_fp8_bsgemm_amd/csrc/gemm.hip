@@ -73,7 +73,6 @@ constexpr int GROUP_M = 4;
 constexpr int NUM_XCD = 8;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 struct GemmArgs {
@@ -911,7 +910,7 @@ __device__ __forceinline__ void lora_add(v4f (&acc)[TM][TN], const GemmArgs &g, 
                 const uint32_t rows = (uint32_t)(mine[i >> 2] >> (16 * (i & 3))) & 0xFFFFu;
                 if (!rows) continue;
                 v8bf hi, lo;
-                lora_load_h(q.lora, mw + 16 * i + frow, (rows >> frow) & 1, r, s, hi, lo);
+                lora_split(lora_load_h(q.lora, mw + 16 * i + frow, (rows >> frow) & 1, r), s, hi, lo);
 #pragma unroll
                 for (int j = 0; j < TN; j++) {
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], hi, acc[i][j], 0, 0, 0);

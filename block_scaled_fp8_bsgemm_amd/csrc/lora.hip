@@ -21,8 +21,6 @@
 
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 // ------------------------------------------------------------------- plan --
 
 // plan = start[0 .. L+1], order[0 .. M): with key(m) = id(m) for an id in
@@ -144,12 +142,12 @@ __device__ __forceinline__ RowTile find_tile(const int32_t *plan, int M, int L, 
 // The most tiles that M rows in L + 1 groups can make.
 inline int64_t max_tiles(int64_t M, int64_t L, int T) { return M / T + (L + 1 < M ? L + 1 : M); }
 
-// The batch row at position p of order; M (no row) outside the tile or for an
-// entry that is no row.
-__device__ __forceinline__ int tile_row(const int32_t *order, const RowTile &t, int i, int M) {
-    if (i >= t.count) return M;
-    const int m = order[t.first + i];
-    return (uint32_t)m < (uint32_t)M ? m : M;
+// The batch row of the tile's row `lane`, one load for the wave; M (no row) past
+// the tile's count or for an entry that is no row.  Any lane's is then had by a
+// shuffle.
+__device__ __forceinline__ int tile_rows(const int32_t *order, const RowTile &t, int lane, int M) {
+    const int m = order[t.first + min(lane, t.count - 1)];
+    return lane < t.count && (uint32_t)m < (uint32_t)M ? m : M;
 }
 
 // ----------------------------------------------------------------- shrink --
@@ -163,11 +161,32 @@ struct ShrinkArgs {
     int64_t K;
 };
 
-// Eight bf16 of a row from k on, zero past its end (K % 8 == 0).
+// Eight bf16 of a row from k on.  TAIL: zero past its end (K % 8 == 0).
+template <bool TAIL>
 __device__ __forceinline__ v8bf load_k(const uint16_t *row, int64_t k, int64_t K) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (k < K) v = *(const u32x4 *)(row + k);
-    return __builtin_bit_cast(v8bf, v);
+    const u32x4 v = *(const u32x4 *)(row + (TAIL && k >= K ? 0 : k));
+    const u32x4 z = {0u, 0u, 0u, 0u};
+    return __builtin_bit_cast(v8bf, TAIL && k >= K ? z : v);
+}
+
+template <int RT, int CT, bool TAIL>
+__device__ __forceinline__ void shrink_step(v4f (&acc)[RT][CT], const uint16_t *const (&xr)[RT],
+                                            const uint16_t *const (&ar)[CT], int64_t k, int64_t K) {
+    v8bf xv[RT][2], av[CT][2];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+        for (int i = 0; i < RT; i++) xv[i][h] = load_k<TAIL>(xr[i], k + 8 * h, K);
+#pragma unroll
+        for (int j = 0; j < CT; j++) av[j][h] = load_k<TAIL>(ar[j], k + 8 * h, K);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+#pragma unroll
+            for (int j = 0; j < CT; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[j][h], xv[i][h], acc[i][j], 0, 0, 0);
 }
 
 // One workgroup: 16 RT rows of one adapter, 16 CT columns of H.  Its W waves
@@ -189,9 +208,10 @@ __global__ void __launch_bounds__(W * 64) lora_shrink_kernel(ShrinkArgs g) {
     if (t.count <= 0) return;
     const int32_t *order = g.plan + g.L + 2;
     const int c0 = blockIdx.y * 16 * CT;
+    const int rows = tile_rows(order, t, lane, g.M);
     int row[RT];
 #pragma unroll
-    for (int i = 0; i < RT; i++) row[i] = tile_row(order, t, 16 * i + fr, g.M);
+    for (int i = 0; i < RT; i++) row[i] = __shfl(rows, 16 * i + fr, 64);
     if (t.group < g.L) {
         const uint16_t *xr[RT], *ar[CT];
 #pragma unroll
@@ -204,25 +224,9 @@ __global__ void __launch_bounds__(W * 64) lora_shrink_kernel(ShrinkArgs g) {
         for (int i = 0; i < RT; i++)
 #pragma unroll
             for (int j = 0; j < CT; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-        for (int64_t k0 = wave * 64; k0 < g.K; k0 += W * 64) {
-            const int64_t k = k0 + 16 * fg;
-            v8bf xv[RT][2], av[CT][2];
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-#pragma unroll
-                for (int i = 0; i < RT; i++) xv[i][h] = load_k(xr[i], k + 8 * h, g.K);
-#pragma unroll
-                for (int j = 0; j < CT; j++) av[j][h] = load_k(ar[j], k + 8 * h, g.K);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int i = 0; i < RT; i++)
-#pragma unroll
-                    for (int j = 0; j < CT; j++)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[j][h], xv[i][h], acc[i][j], 0, 0, 0);
-        }
+        int64_t k0 = wave * 64;
+        for (; k0 + 64 <= g.K; k0 += W * 64) shrink_step<RT, CT, false>(acc, xr, ar, k0 + 16 * fg, g.K);
+        if (k0 < g.K) shrink_step<RT, CT, true>(acc, xr, ar, k0 + 16 * fg, g.K);
 #pragma unroll
         for (int i = 0; i < RT; i++)
 #pragma unroll
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(W * 64) lora_shrink_kernel(ShrinkArgs g) {
             for (int w = 0; w < W; w++) sum += part[w][s][lane];
         }
         const int c = c0 + 16 * (s % CT) + 4 * fg;
-        const int m = tile_row(order, t, 16 * (s / CT) + fr, g.M);
+        const int m = __shfl(rows, 16 * (s / CT) + fr, 64);
         if (m < g.M && c < g.R) *(v4f *)(g.H + (int64_t)m * g.R + c) = sum;
     }
 }
@@ -248,17 +252,37 @@ struct ExpandArgs {
     const int32_t *plan;
     const uint16_t *base;   // bf16 row bands
     uint16_t *out;
-    int M, col_blocks;
-    int64_t N, band_rows, band_stride;
+    int M, band_rows;
+    int col_blocks, chunks;   // workgroups along N, and 256-column chunks to each
+    int64_t N, band_gap;
 };
 
-// One workgroup: 16 RT rows of one adapter, 256 columns, 64 to a wave.  The
-// B rows are the MFMA's first operand, its fragment rows taken in the order
-// of lora_col, so that a lane holds 8 consecutive columns of a row in each
-// half of the wave's 64 and moves base and out in 16-byte pieces.  base is
-// loaded before the products and added to them in fp32; out is rounded once.
-template <int RT>
+// Lanes l and l ^ 8 exchange v (a DPP rotation by 8 within each 16 lanes).
+__device__ __forceinline__ u32x4 swap8(u32x4 v) {
+    u32x4 r;
+#pragma unroll
+    for (int e = 0; e < 4; e++) r[e] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[e], 0x128, 0xF, 0xF, false);
+    return r;
+}
+
+// One workgroup: 16 RT rows of one adapter and `chunks` column chunks of 256,
+// 64 columns to a wave.  The rows' scale * H is split into its two bf16 once
+// and kept in LDS for all of them: row i is 2 NCH 16-byte pieces, hi's pieces
+// 0 .. NCH - 1 before lo's, each at its number xor (i mod 16), so that the 16 rows
+// of a fragment read lie in different banks.
+//
+// The B rows are the MFMA's first operand, its fragment rows taken in the order
+// of lora_col, so that lane l = r + 16 g holds 16-byte pieces g and 4 + g of
+// row r's 128 bytes.  base and out move in whole 128-byte row segments, eight
+// rows to an instruction: X covers rows 0..7 of a 16-row group, lanes r < 8
+// piece g and lanes r >= 8 piece 4 + g of row r % 8, and Y rows 8..15 with the
+// pieces the other way round; one exchange between lanes l and l ^ 8 goes from
+// either form to the other.  base is loaded before the products and added to
+// them in fp32; out is rounded once.
+template <int RT, int RMAX>
 __global__ void __launch_bounds__(256) lora_expand_kernel(ExpandArgs g) {
+    constexpr int NCH = RMAX / 8;
+    __shared__ u32x4 sh[16 * RT * 2 * NCH];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fg = lane >> 4;
@@ -267,63 +291,104 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(ExpandArgs g) {
     if (t.count <= 0) return;
     const bool has = t.group < g.lora.L;
     if (!has && g.base == g.out) return;   // rows without an adapter, in place
-    const int32_t *order = g.plan + g.lora.L + 2;
-    const int64_t n0 = (int64_t)((int)blockIdx.x - tile * g.col_blocks) * 256 + wave * 64;
-    int row[RT];
-    int64_t at[RT];
-    u32x4 bv[RT][2];
-#pragma unroll
-    for (int i = 0; i < RT; i++) {
-        row[i] = tile_row(order, t, 16 * i + fr, g.M);
-        const int64_t band = row[i] / g.band_rows;
-        at[i] = band * g.band_stride + (row[i] - band * g.band_rows) * g.N + n0 + 8 * fg;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            bv[i][h] = (u32x4){0u, 0u, 0u, 0u};
-            if (row[i] < g.M && n0 + 8 * fg + 32 * h < g.N)
-                bv[i][h] = __builtin_nontemporal_load((const u32x4 *)(g.base + at[i] + 32 * h));
-        }
-    }
-    v4f acc[RT][4];
-#pragma unroll
-    for (int i = 0; i < RT; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+    const int rows = tile_rows(g.plan + g.lora.L + 2, t, lane, g.M);
     if (has) {
         const float s = g.lora.scale ? g.lora.scale[t.group] : 1.0f;
-        const uint16_t *br[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) br[j] = lora_brow(g.lora, t.group, n0 + lora_col(j, fr), g.N);
-        for (int r0 = 0; r0 < g.lora.R; r0 += 32) {
-            const int r = r0 + 8 * fg;
-            v8bf b[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) b[j] = lora_load_b(br[j], r, g.lora.R);
-#pragma unroll
-            for (int i = 0; i < RT; i++) {
-                v8bf hi, lo;
-                lora_load_h(g.lora, row[i], row[i] < g.M, r, s, hi, lo);
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], hi, acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], lo, acc[i][j], 0, 0, 0);
-                }
-            }
+        for (int k = 0; k < (16 * RT * NCH + 255) / 256; k++) {
+            const int i = (threadIdx.x + 256 * k) / NCH, c = threadIdx.x % NCH;
+            if (i >= 16 * RT) break;   // whole waves: NCH divides 64
+            const int m = __shfl(rows, i, 64);
+            v8bf hi, lo;
+            lora_split(lora_load_h(g.lora, m, m < g.M, 8 * c), s, hi, lo);
+            sh[i * 2 * NCH + (c ^ (i & 15))] = __builtin_bit_cast(u32x4, hi);
+            sh[i * 2 * NCH + ((NCH + c) ^ (i & 15))] = __builtin_bit_cast(u32x4, lo);
         }
+        __syncthreads();
     }
+    const bool up = fr >= 8;
+    int64_t at[RT][2];     // first element of the X and Y rows; negative: no row
 #pragma unroll
     for (int i = 0; i < RT; i++)
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            if (row[i] >= g.M || n0 + 8 * fg + 32 * h >= g.N) continue;
-            u32x4 o;
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const v4f &c = acc[i][2 * h + (e >> 1)];
-                o[e] = pack_bf16x2(bf16_lo(bv[i][h][e]) + c[2 * (e & 1)], bf16_hi(bv[i][h][e]) + c[2 * (e & 1) + 1]);
-            }
-            __builtin_nontemporal_store(has ? o : bv[i][h], (u32x4 *)(g.out + at[i] + 32 * h));
+            const int m = __shfl(rows, 16 * i + 8 * h + (fr & 7), 64);
+            // band_gap: what a band's stride has beyond its rows
+            const int64_t gap = g.band_gap ? g.band_gap * ((uint32_t)m / (uint32_t)g.band_rows) : 0;
+            at[i][h] = m < g.M ? m * g.N + gap : -1;
         }
+    const int64_t first = (int64_t)((int)blockIdx.x - tile * g.col_blocks) * g.chunks;
+    const int64_t end = min((first + g.chunks) * 256, g.N);
+    const int dx = 8 * fg + (up ? 32 : 0), dy = 8 * fg + (up ? 0 : 32);
+    auto load_b = [&](v8bf(&b)[4], int64_t n, int r0) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            b[j] = lora_load_b(lora_brow(g.lora, t.group, n + lora_col(j, fr), g.N), r0 + 8 * fg, g.lora.R);
+    };
+    v8bf bnext[4];
+    if (has) load_b(bnext, first * 256 + wave * 64, 0);
+    for (int64_t n0 = first * 256 + wave * 64; n0 < end; n0 += 256) {
+        u32x4 xy[RT][2];   // base's pieces (anything where there are none)
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int64_t n = n0 + (h ? dy : dx);
+                xy[i][h] = __builtin_nontemporal_load(
+                    (const u32x4 *)(g.base + (at[i][h] >= 0 && n < g.N ? at[i][h] + n : 0)));
+            }
+        if (has) {
+            v4f acc[RT][4];
+#pragma unroll
+            for (int i = 0; i < RT; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+            for (int r0 = 0; r0 < g.lora.R; r0 += 32) {
+                const int r = r0 + 8 * fg;
+                v8bf b[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) b[j] = bnext[j];
+                const bool last = r0 + 32 >= g.lora.R;
+                load_b(bnext, last ? n0 + 256 : n0, last ? 0 : r0 + 32);
+#pragma unroll
+                for (int i = 0; i < RT; i++) {
+                    const u32x4 *row = sh + (16 * i + fr) * 2 * NCH;
+                    const v8bf hi = __builtin_bit_cast(v8bf, row[(r / 8) ^ fr]);
+                    const v8bf lo = __builtin_bit_cast(v8bf, row[(NCH + r / 8) ^ fr]);
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], hi, acc[i][j], 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], lo, acc[i][j], 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RT; i++) {
+                const u32x4 lo = up ? xy[i][1] : xy[i][0], hi = swap8(up ? xy[i][0] : xy[i][1]);
+                u32x4 o[2];
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const uint32_t w = h ? hi[e] : lo[e];
+                        const v4f &c = acc[i][2 * h + (e >> 1)];
+                        o[h][e] = pack_bf16x2(bf16_lo(w) + c[2 * (e & 1)], bf16_hi(w) + c[2 * (e & 1) + 1]);
+                    }
+                const u32x4 oh = swap8(o[1]);
+                xy[i][0] = up ? oh : o[0];
+                xy[i][1] = up ? o[0] : oh;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int64_t n = n0 + (h ? dy : dx);
+                if (at[i][h] >= 0 && n < g.N)
+                    __builtin_nontemporal_store(xy[i][h], (u32x4 *)(g.out + at[i][h] + n));
+            }
+    }
 }
 
 }  // namespace
@@ -335,14 +400,41 @@ int bs_launch_lora_plan(const int32_t *ids, int32_t *plan, int64_t M, int L, hip
 int bs_launch_lora_shrink(const uint16_t *x, const uint16_t *A, const int32_t *plan, float *H, int64_t M, int64_t K,
                           int L, int R, hipStream_t stream) {
     const ShrinkArgs g = {x, A, plan, H, (int)M, L, R, K};
+    if (M >= 64 * (int64_t)(L + 1)) {
+        const dim3 grid((unsigned)max_tiles(M, L, 32), (unsigned)((R + 63) / 64));
+        return bs_enqueue(lora_shrink_kernel<2, 4, 4>, grid, dim3(256), stream, g);
+    }
     const dim3 grid((unsigned)max_tiles(M, L, 16), (unsigned)((R + 63) / 64));
     return bs_enqueue(lora_shrink_kernel<1, 4, 8>, grid, dim3(512), stream, g);
 }
 
+template <int RT, int RMAX>
+static int launch_expand(ExpandArgs g, hipStream_t stream) {
+    const int64_t cols = (g.N + 255) / 256, tiles = max_tiles(g.M, g.lora.L, 16 * RT);
+    // A workgroup takes as many column chunks as leave about 1024 of them, two rounds
+    // of the 512 that the registers let a device hold at RT = 4: a long run of
+    // chunks pays for finding the tile and splitting its H once.  M = 16384,
+    // N = 5120, 8 adapters of rank 32 / 64 / 128: 79.6 / 86.8 / 104.9 us, against
+    // 84.5 / 87.1 / 103.4 at 512 workgroups, 80.5 / 92.0 / 111.8 at 2048 and 90.0 /
+    // 97.4 / 117.8 at one chunk to each.
+    int64_t chunks = tiles * cols / 1024;
+    chunks = chunks < 1 ? 1 : chunks > cols ? cols : chunks;
+    g.chunks = (int)chunks;
+    g.col_blocks = (int)((cols + chunks - 1) / chunks);
+    if (tiles * g.col_blocks > 0x7FFFFFFF) return -1;
+    return bs_enqueue(lora_expand_kernel<RT, RMAX>, dim3((unsigned)(tiles * g.col_blocks)), dim3(256), stream, g);
+}
+
+template <int RT>
+static int launch_expand_r(const ExpandArgs &g, hipStream_t stream) {
+    if (g.lora.R <= 64) return launch_expand<RT, 64>(g, stream);
+    if (g.lora.R <= 128) return launch_expand<RT, 128>(g, stream);
+    return launch_expand<RT, 256>(g, stream);
+}
+
 int bs_launch_lora_expand(const LoraArgs &lora, const int32_t *plan, const uint16_t *base, uint16_t *out, int64_t M,
                           int64_t N, int64_t band_rows, int64_t band_stride, hipStream_t stream) {
-    const int64_t cols = (N + 255) / 256, blocks = max_tiles(M, lora.L, 16) * cols;
-    if (blocks > 0x7FFFFFFF) return -1;
-    const ExpandArgs g = {lora, plan, base, out, (int)M, (int)cols, N, band_rows, band_stride};
-    return bs_enqueue(lora_expand_kernel<1>, dim3((unsigned)blocks), dim3(256), stream, g);
+    const ExpandArgs g = {lora, plan, base, out, (int)M, (int)band_rows, 0, 0, N, band_stride - band_rows * N};
+    if (M >= 64 * (int64_t)(lora.L + 1)) return launch_expand_r<4>(g, stream);
+    return launch_expand_r<1>(g, stream);
 }

@@ -29,26 +29,37 @@ __device__ __forceinline__ const uint16_t *lora_brow(const LoraArgs &g, int a, i
     return g.B + ((int64_t)a * N + (n < N ? n : N - 1)) * g.R;
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Loads whose lanes may have nothing to load take a valid address all the same
+// and select zero afterwards: a branch around each load would keep the compiler from
+// issuing them together.
 __device__ __forceinline__ v8bf lora_load_b(const uint16_t *row, int r, int R) {
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (r < R) v = *(const u32x4 *)(row + r);
-    return __builtin_bit_cast(v8bf, v);
+    const u32x4 v = *(const u32x4 *)(row + (r < R ? r : 0));
+    const u32x4 z = {0u, 0u, 0u, 0u};
+    return __builtin_bit_cast(v8bf, r < R ? v : z);
 }
 
 // scale * H[m, r .. r+8) split in two; zero for a row that is not the
 // adapter's (live == false) and past R.
-__device__ __forceinline__ void lora_load_h(const LoraArgs &g, int64_t m, bool live, int r, float s, v8bf &hi,
-                                            v8bf &lo) {
-    v4f a = {0.f, 0.f, 0.f, 0.f}, b = {0.f, 0.f, 0.f, 0.f};
-    if (live && r < g.R) {
-        const v4f *p = (const v4f *)(g.H + m * g.R + r);
-        a = p[0];
-        b = p[1];
+struct LoraH {
+    v4f a, b;
+};
+__device__ __forceinline__ LoraH lora_load_h(const LoraArgs &g, int64_t m, bool live, int r) {
+    const bool ok = live && r < g.R;
+    const v4f *p = (const v4f *)(g.H + (ok ? m * g.R + r : 0));
+    LoraH h = {p[0], p[1]};
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        h.a[e] = ok ? h.a[e] : 0.f;
+        h.b[e] = ok ? h.b[e] : 0.f;
     }
+    return h;
+}
+__device__ __forceinline__ void lora_split(const LoraH &h, float s, v8bf &hi, v8bf &lo) {
 #pragma unroll
     for (int e = 0; e < 8; e++) {
-        const float v = s * (e < 4 ? a[e & 3] : b[e & 3]);
+        const float v = s * (e < 4 ? h.a[e & 3] : h.b[e & 3]);
         hi[e] = (__bf16)v;
         lo[e] = (__bf16)(v - (float)hi[e]);
     }
