@@ -569,8 +569,10 @@ __device__ __forceinline__ void kblock_pb(v4f (&acc)[TM][TN], v4f (&p)[4], float
 // The block loaded is block kload of the panels P, moved by d to another
 // tile: the persistent kernel's last block of a tile loads the next tile's
 // block 0, whose head it then reads.  After the last tile the DMA goes
-// nowhere and those reads fetch unused values.
-template <int ST, int SHIFT = 0>
+// nowhere and those reads fetch unused values.  NEXT = false leaves both out:
+// the other stage is then filled by the caller (the adapters' H, before this
+// block) and waited for at the barrier.
+template <int ST, int SHIFT = 0, bool NEXT = true>
 __device__ __forceinline__ void kblock(v4f (&acc)[TM][TN], v4f (&p)[4], float &s_tail, v8i &a,
                                        v8i (&bf)[TN], float (&s)[TM], const Loader &L,
                                        const Panels &P, int kload, bool vload, int wm, int wn,
@@ -585,8 +587,10 @@ __device__ __forceinline__ void kblock(v4f (&acc)[TM][TN], v4f (&p)[4], float &s
         if (i + 1 < TM) an = lds_frag(as, wm * WM + (i + 1) * 16 + frow, fc);
         if (i == TM - 1) {
             wait_dma_and_sync();
-            a_next = lds_frag(stA<ST ^ 1>(), wm * WM + frow, fc);
-            read_scales<ST ^ 1>(rn, wm, wn, frow);
+            if constexpr (NEXT) {
+                a_next = lds_frag(stA<ST ^ 1>(), wm * WM + frow, fc);
+                read_scales<ST ^ 1>(rn, wm, wn, frow);
+            }
         }
 #pragma unroll
         for (int j = 0; j < TN; j++) {
@@ -600,19 +604,19 @@ __device__ __forceinline__ void kblock(v4f (&acc)[TM][TN], v4f (&p)[4], float &s
                 // products 29, 30, 31 of the previous block: row group 7
                 fold4(acc[TM - 1][k + 1], p[(k + 1) & 3], s_tail);
             }
-            if (i == TM - 1) {
+            if (NEXT && i == TM - 1) {
                 bf[j] = lds_frag(stB<ST ^ 1>(), wn * WN + j * 16 + frow, fc);
             }
             // the DMA of the next block (kload, normally kb + 1) into the
             // other stage (unread since the previous block's barrier), one
             // instruction after each of nine consecutive MFMAs from MFMA
             // SHIFT on, away from the head reads of row group 7
-            if (k >= SHIFT) dma_block<ST>(L, P, k - SHIFT, kload, vload, d);
+            if (NEXT && k >= SHIFT) dma_block<ST>(L, P, k - SHIFT, kload, vload, d);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
     s_tail = s[TM - 1];
-    combine_scales(s, rn);
+    if constexpr (NEXT) combine_scales(s, rn);
     a = a_next;
 }
 
@@ -866,58 +870,220 @@ struct LoraGemmArgs {
 };
 
 // Adds scale[a] (H[m] B[a]^T), a = ids[m], to the finished accumulators of a
-// wave's 128 x 64 sub-tile, in fp32, before the one rounding to bf16.  A wave
-// goes through the distinct adapters of its 128 rows (one or two in a prefill
-// chunk, whose requests are runs of rows).  For each it loads the adapter's 64
-// columns of B once per 32 of R, in the sub-tiles' own column order, and gives
-// every 16-row group that has such a row its products, with H zero in the rows
-// of other adapters.  A group without one is skipped, so a row of no adapter
+// tile, in fp32, before the one rounding to bf16.
+//
+// 64 ranks at a time: the tile's 256 rows of H come by DMA into a stage, 32
+// ranks (128 bytes a row) into its A part and 32 into its B part, in the row
+// slots of the A tile.  The first 64 go to stage 1 during the last K block,
+// which takes no next block there; later ones to the two stages in turn, during the
+// products of those before.  A wave then turns the rows it loaded into scale *
+// value split in two bf16, in place: of every two 16-byte chunks, eight ranks,
+// the first gets the hi parts and the second the lo parts.  So the split is done
+// once for the four waves that share the rows.
+//
+// A wave goes through the distinct adapters of its 128 rows (one or two in a
+// prefill chunk, whose requests are runs of rows).  For each it has the
+// adapter's 64 columns of B in registers, in the sub-tiles' own column order, and gives every
+// 16-row group that has such a row its products, with zeros in the rows of
+// other adapters.  A group without one is skipped, so a row of no adapter
 // keeps its product bit for bit unless it shares a group with others', where
 // it gets a zero added, which changes nothing but the sign of a zero.
-__device__ __forceinline__ void lora_add(v4f (&acc)[TM][TN], const GemmArgs &g, const LoraGemmArgs &q, int64_t m0,
-                                         int64_t n0, int wm, int wn, int lane) {
-    const int frow = lane & 15, fg = lane >> 4;
-    const int64_t mw = m0 + wm * WM;
-    int id[2];
-    uint64_t todo[2];
+
+// ids of the tile's rows, loaded with the tile's first K block
+__shared__ int32_t sI[BM];
+
+// Waves 0..3 take 64 each; rows past M read as 0 and are told apart by their number.
+__device__ __forceinline__ void load_ids(const GemmArgs &g, const LoraGemmArgs &q, int64_t m0, int wave, int lane) {
+    if (wave < 4)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(q.ids + m0, (g.M - m0 < BM ? g.M - m0 : BM) * 4),
+                                                 (lds_void *)&sI[wave * 64], 4, (wave * 64 + lane) * 4, 0, 0, 0);
+}
+
+// A tile row's adapter, -1 if it has none.
+__device__ __forceinline__ int id_of(const GemmArgs &g, const LoraGemmArgs &q, int64_t m0, int r) {
+    const int a = sI[r];
+    return m0 + r < g.M && (uint32_t)a < (uint32_t)q.lora.L ? a : -1;
+}
+
+__device__ __forceinline__ bool tile_has_adapter(const GemmArgs &g, const LoraGemmArgs &q, int64_t m0, int lane) {
+    bool has = false;
+#pragma unroll
+    for (int h = 0; h < 4; h++) has |= id_of(g, q, m0, 64 * h + lane) >= 0;
+    return __ballot(has) != 0;
+}
+
+// Brings the tile's rows of H, and of B of its first adapter, into L2 while the
+// K loop runs: a lane reads one word of half a row of each and drops it.
+struct LoraTouch {
+    uint32_t b, h;
+};
+__device__ __forceinline__ LoraTouch lora_touch(const GemmArgs &g, const LoraGemmArgs &q, int64_t m0, int64_t n0,
+                                                int tid, int lane) {
+    int a = -1;
+#pragma unroll
+    for (int h = 0; h < 4; h++) {
+        const int id = id_of(g, q, m0, 64 * h + lane);
+        const uint64_t has = __ballot(id >= 0);
+        if (a < 0 && has) a = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)has) - 1);
+    }
+    const int64_t m = min(m0 + (tid >> 1), g.M - 1);
+    const int half = (tid & 1) * (q.lora.R / 2);
+    LoraTouch t;
+    t.b = *(const uint32_t *)(lora_brow(q.lora, a, n0 + (tid >> 1), g.N) + half);
+    t.h = __float_as_uint(q.lora.H[m * q.lora.R + half]);
+    return t;
+}
+
+// H's ranks rc .. rc+63 into stage ST: slot i of wave w as in load_stage; a chunk
+// past R goes out of the descriptor's range and reads as zero.
+template <int ST>
+__device__ __forceinline__ void lora_dma(const GemmArgs &g, const LoraGemmArgs &q, int64_t m0, int rc, int wave,
+                                         int lane) {
+    asm volatile("" : "+v"(lane));   // addresses formed here, not hoisted
+    const int R = q.lora.R;
+    const __amdgpu_buffer_rsrc_t rH = make_rsrc(q.lora.H + m0 * R, (g.M - m0 < BM ? g.M - m0 : BM) * R * 4);
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-        const int64_t m = mw + 64 * h + lane;
-        id[h] = -1;
-        if (m < g.M) {
-            const int a = q.ids[m];
-            if ((uint32_t)a < (uint32_t)q.lora.L) id[h] = a;
+        if (rc + 32 * h >= R) break;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int row = wave * 32 + (lane >> 4) + 8 * ((lane >> 3) & 1) + 16 * (i >> 1) + 4 * (i & 1);
+            const int r = rc + 32 * h + 4 * ((lane & 7) ^ (lane >> 4) ^ (4 * (i & 1)));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rH, (lds_void *)((h ? stB<ST>() : stA<ST>()) + wave * 4096 + i * 1024), 16,
+                r < R ? (row * R + r) * 4 : 0x7FFFFFF0, 0, 0, 0);
         }
-        todo[h] = __ballot(id[h] >= 0);
     }
-    while (todo[0] | todo[1]) {
-        const int a = todo[0] ? __builtin_amdgcn_readlane(id[0], __ffsll((unsigned long long)todo[0]) - 1)
-                              : __builtin_amdgcn_readlane(id[1], __ffsll((unsigned long long)todo[1]) - 1);
-        const uint64_t mine[2] = {__ballot(id[0] == a), __ballot(id[1] == a)};
+}
+
+// One lane's 32 values of a row: the row's 128 bytes in st, split in place.
+__device__ __forceinline__ void lora_split_row(uint8_t *st, int r, float s) {
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        u32x4 *p0 = (u32x4 *)(st + swz(r, 2 * c)), *p1 = (u32x4 *)(st + swz(r, 2 * c + 1));
+        LoraH h;
+        h.a = __builtin_bit_cast(v4f, *p0);
+        h.b = __builtin_bit_cast(v4f, *p1);
+        v8bf hi, lo;
+        lora_split(h, s, hi, lo);
+        *p0 = __builtin_bit_cast(u32x4, hi);
+        *p1 = __builtin_bit_cast(u32x4, lo);
+    }
+}
+
+// A wave's adapters: of its 128 rows, and the first one's B, which is loaded a
+// step ahead.
+struct LoraWave {
+    int id[2];       // adapters of rows lane and 64 + lane
+    int first;       // the first of them
+    v8bf b0[TN];     // its B for the coming ranks rc .. rc+31
+};
+
+// Half h of ranks rc .. rc+63 of adapter a's B, for the wave's columns from n on;
+// past R, and past N, the offset is out of the descriptor's range and reads as zero.
+__device__ __forceinline__ void lora_b(v8bf (&b)[TN], const GemmArgs &g, const LoraGemmArgs &q, int a, int64_t n,
+                                       int rc, int h, int lane) {
+    const int R = q.lora.R, r = rc + 32 * h + 8 * (lane >> 4);
+    if (rc + 32 * h >= R) return;
+    const __amdgpu_buffer_rsrc_t rB =
+        make_rsrc(q.lora.B + ((int64_t)a * g.N + n) * R, (g.N - n < WN ? g.N - n : WN) * R * 2);
+#pragma unroll
+    for (int j = 0; j < TN; j++)
+        b[j] = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(
+                                            rB, r < R ? (lora_col(j, lane & 15) * R + r) * 2 : 0x7FFFFFF0, 0, 0));
+}
+
+__device__ __forceinline__ int lora_first(const int (&id)[2], const uint64_t (&todo)[2]) {
+    return todo[0] ? __builtin_amdgcn_readlane(id[0], __ffsll((unsigned long long)todo[0]) - 1)
+                   : __builtin_amdgcn_readlane(id[1], __ffsll((unsigned long long)todo[1]) - 1);
+}
+
+__device__ __forceinline__ void lora_begin(LoraWave &w, const GemmArgs &g, const LoraGemmArgs &q, int64_t m0,
+                                           int64_t n, int wm, int lane) {
+    w.id[0] = id_of(g, q, m0, wm * WM + lane);
+    w.id[1] = id_of(g, q, m0, wm * WM + 64 + lane);
+    const uint64_t all[2] = {__ballot(w.id[0] >= 0), __ballot(w.id[1] >= 0)};
+    w.first = -1;
+    if (all[0] | all[1]) {
+        w.first = lora_first(w.id, all);
+        lora_b(w.b0, g, q, w.first, n, 0, 0, lane);
+    }
+}
+
+// The products of ranks rc .. rc+63, whose H is in stage ST.
+template <int ST>
+__device__ __forceinline__ void lora_chunk(v4f (&acc)[TM][TN], LoraWave &w, const GemmArgs &g, const LoraGemmArgs &q,
+                                           float cs, int64_t n, int rc, int wm, int wave, int lane) {
+    const int frow = lane & 15, fg = lane >> 4;
+    const int R = q.lora.R;
+    v8bf b1[TN];
+    if (w.first >= 0) lora_b(b1, g, q, w.first, n, rc, 1, lane);
+    // the first 32 lanes take the A part's rows, the others the B part's, of the
+    // rows this wave loaded
+    const int crow = wave * 32 + (lane & 31);
+    if (lane < 32) lora_split_row(stA<ST>(), crow, cs);
+    else if (rc + 32 < R) lora_split_row(stB<ST>(), crow, cs);
+    barrier_lds_only();
+    auto half = [&](int h, const v8bf(&b)[TN], const uint64_t (&mine)[2]) {
+        if (rc + 32 * h >= R) return;
+#pragma unroll
+        for (int i = 0; i < TM; i++) {
+            const uint32_t rows = (uint32_t)(mine[i >> 2] >> (16 * (i & 3))) & 0xFFFFu;
+            if (!rows) continue;
+            const bool live = (rows >> frow) & 1;
+            const uint8_t *st = h ? stB<ST>() : stA<ST>();
+            const int r = wm * WM + 16 * i + frow;
+            u32x4 hi = *(const u32x4 *)(st + swz(r, 2 * fg)), lo = *(const u32x4 *)(st + swz(r, 2 * fg + 1));
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                hi[e] = live ? hi[e] : 0u;
+                lo[e] = live ? lo[e] : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < TN; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, hi), acc[i][j], 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < TN; j++)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, lo), acc[i][j], 0, 0, 0);
+        }
+    };
+    if (w.first < 0) return;
+    uint64_t todo[2] = {__ballot(w.id[0] >= 0), __ballot(w.id[1] >= 0)};
+    int a = w.first;
+    for (;;) {
+        const uint64_t mine[2] = {__ballot(w.id[0] == a), __ballot(w.id[1] == a)};
         todo[0] &= ~mine[0];
         todo[1] &= ~mine[1];
-        const float s = q.lora.scale ? q.lora.scale[a] : 1.0f;
-        const uint16_t *br[TN];
-#pragma unroll
-        for (int j = 0; j < TN; j++) br[j] = lora_brow(q.lora, a, n0 + wn * WN + lora_col(j, frow), g.N);
-        for (int r0 = 0; r0 < q.lora.R; r0 += 32) {
-            const int r = r0 + 8 * fg;
-            v8bf b[TN];
-#pragma unroll
-            for (int j = 0; j < TN; j++) b[j] = lora_load_b(br[j], r, q.lora.R);
-#pragma unroll
-            for (int i = 0; i < TM; i++) {
-                const uint32_t rows = (uint32_t)(mine[i >> 2] >> (16 * (i & 3))) & 0xFFFFu;
-                if (!rows) continue;
-                v8bf hi, lo;
-                lora_split(lora_load_h(q.lora, mw + 16 * i + frow, (rows >> frow) & 1, r), s, hi, lo);
-#pragma unroll
-                for (int j = 0; j < TN; j++) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], hi, acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], lo, acc[i][j], 0, 0, 0);
-                }
-            }
-        }
+        const bool more = (todo[0] | todo[1]) != 0;
+        half(0, w.b0, mine);
+        // a half's registers are free for what comes next: the next adapter, or the
+        // first one's next ranks
+        if (more) a = lora_first(w.id, todo);
+        lora_b(w.b0, g, q, more ? a : w.first, n, more ? rc : rc + 64, 0, lane);
+        half(1, b1, mine);
+        if (!more) break;
+        lora_b(b1, g, q, a, n, rc, 1, lane);
+    }
+}
+
+// All ranks; the first 64 are in stage 1, and every wave has passed a barrier since.
+__device__ __forceinline__ void lora_add(v4f (&acc)[TM][TN], const GemmArgs &g, const LoraGemmArgs &q, int64_t m0,
+                                         int64_t n, int wm, int wave, int lane) {
+    asm volatile("" : "+v"(lane));   // addresses formed here, not hoisted
+    LoraWave w;
+    lora_begin(w, g, q, m0, n, wm, lane);
+    const int R = q.lora.R;
+    float cs = 1.0f;   // the scale of the row this lane splits
+    if (q.lora.scale) cs = q.lora.scale[max(id_of(g, q, m0, wave * 32 + (lane & 31)), 0)];
+    for (int rc = 0;;) {
+        if (rc + 64 < R) lora_dma<0>(g, q, m0, rc + 64, wave, lane);
+        lora_chunk<1>(acc, w, g, q, cs, n, rc, wm, wave, lane);
+        if ((rc += 64) >= R) return;
+        wait_dma_and_sync();   // the next ranks are in, and these are read
+        if (rc + 64 < R) lora_dma<1>(g, q, m0, rc + 64, wave, lane);
+        lora_chunk<0>(acc, w, g, q, cs, n, rc, wm, wave, lane);
+        if ((rc += 64) >= R) return;
+        wait_dma_and_sync();
     }
 }
 
@@ -936,6 +1102,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
     const int KB = g.KB;
     constexpr bool MX = MODE == MODE_MX;
 
+    if constexpr (LORA) load_ids(g, q, m0, wave, lane);
+    bool any = false;   // whether a row of the tile has an adapter
     Loader L;
     init_loader<MODE>(L, g, wave, lane);
     L.P = panels_of<MODE>(g, m0, n0, wave);
@@ -1016,6 +1184,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
         read_head<1>(a, bf, s, wm, wn, frow, fc);
     }
 
+    LoraTouch touch = {0u, 0u};
+    if constexpr (LORA) {
+        any = tile_has_adapter(g, q, m0, lane);
+        if (any) touch = lora_touch(g, q, m0, n0, tid, lane);
+    }
     // nothing pending before the first block: its first three folds add 0 * 0
     v4f p[4];
 #pragma unroll
@@ -1027,16 +1200,29 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
         kblock<0>(acc, p, s_tail, a, bf, s, L, L.P, 1, 1 < KB, wm, wn, frow, fc);
         kb = 1;
     }
-    for (; kb < KB; kb += 2) {
+    for (; kb < KB - (LORA ? 2 : 0); kb += 2) {
         kblock<1>(acc, p, s_tail, a, bf, s, L, L.P, kb + 1, kb + 1 < KB, wm, wn, frow, fc);
         kblock<0>(acc, p, s_tail, a, bf, s, L, L.P, kb + 2, kb + 2 < KB, wm, wn, frow, fc);
+    }
+    if constexpr (LORA) {
+        asm volatile("" ::"v"(touch.b), "v"(touch.h));
+        if (kb < KB) {   // the last two blocks, the second without a successor
+            kblock<1>(acc, p, s_tail, a, bf, s, L, L.P, kb + 1, true, wm, wn, frow, fc);
+            if (any) lora_dma<1>(g, q, m0, 0, wave, lane);
+            kblock<0, 0, false>(acc, p, s_tail, a, bf, s, L, L.P, 0, false, wm, wn, frow, fc);
+        } else if (any) {   // K = 128: nothing to hide the load behind
+            lora_dma<1>(g, q, m0, 0, wave, lane);
+            wait_dma_and_sync();
+        }
     }
 #pragma unroll
     for (int j = 1; j < TN; j++) fold4(acc[TM - 1][j], p[(TM * TN - TN + j) & 3], s_tail);
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the last (empty) DMA is retired
 
-    if constexpr (LORA) lora_add(acc, g, q, m0, n0, wm, wn, lane);
+    if constexpr (LORA) {
+        if (any) lora_add(acc, g, q, m0, n0 + wn * WN, wm, wave, lane);
+    }
     store_tile<MODE>(acc, g, m0, n0, wave, lane);
 }
 
