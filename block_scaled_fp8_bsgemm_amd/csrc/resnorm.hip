@@ -51,19 +51,18 @@ __device__ __forceinline__ u32x4 narrow(const float (&v)[8]) {
     return o;
 }
 
-// The sum over the T lanes of a row (T = 64: one wave, no LDS).  A second use
-// of red needs no barrier of its own after the first one's reads: it takes
+// The sum over a row's lanes: one wave (WAVE), or the workgroup's waves through
+// red.  A second use needs no barrier after the first one's reads: it takes
 // another slot.
-template <int T>
+template <bool WAVE>
 __device__ __forceinline__ float row_sum(float v, float *red) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-    if constexpr (T > 64) {
+    if constexpr (!WAVE) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
         __syncthreads();
         v = 0.f;
-#pragma unroll
-        for (int w = 0; w < T / 64; w++) v += red[w];
+        for (unsigned w = 0; w < blockDim.x / 64; w++) v += red[w];
     }
     return v;
 }
@@ -76,78 +75,91 @@ __device__ __forceinline__ float group_max(float m) {
     return m;
 }
 
-// T lanes per row, CPT packs of 8 values to a lane (pack tid + T i): rows of
-// up to 8 T CPT values.  WIRE: y is e4m3 codes with a row scale.  RES32: the
-// residual stream is fp32.  QB: 0, or the scale block of q.
-template <int T, int CPT, bool WIRE, bool RES32, int QB>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) resnorm_kernel(ResnormArgs g) {
-    constexpr int ROWS = T < 256 ? 256 / T : 1;
-    __shared__ float red[2][T / 64];
-    const int tid = threadIdx.x % T;
-    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / T;
-    if (row >= g.rows) return;   // whole waves: T >= 64
+// CPT packs of 8 values to a lane.  WAVE: a wave takes a row of up to 64 CPT
+// packs, four rows to a workgroup; otherwise the workgroup's T lanes take one of
+// up to T CPT (lane t the packs t + T i).  WIRE: y is e4m3 codes with a row scale.
+// RES32: the residual stream is fp32.  QB: 0, or the scale block of q.
+//
+// Every load, the weights' and the gate's too, goes out before the first
+// reduction.  A lane past the row's end loads the last pack, counts as zero and
+// stores nothing, so that no load is behind a branch.
+template <int CPT, bool WAVE, bool WIRE, bool RES32, int QB>
+__global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
+    __shared__ float red[2][8];
+    const int T = WAVE ? 64 : (int)blockDim.x;
+    const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if (row >= g.rows) return;   // whole waves of a WAVE workgroup
     const int64_t base = row * g.nch;
     const float inv_n = 1.0f / (float)(g.nch * 8);
 
-    float v[CPT][8], r[CPT][8];
+    u32x4 yw[CPT], ra[CPT], rb[CPT], pw[CPT], gw[CPT], ww[CPT];
+    const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};   // bf16 1.0
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
-        const int c = tid + T * i;
-#pragma unroll
-        for (int e = 0; e < 8; e++) v[i][e] = r[i][e] = 0.f;
-        if (c >= g.nch) continue;
-        if constexpr (WIRE) decode(__builtin_nontemporal_load((const u32x2 *)g.y + base + c), v[i]);
-        else widen(__builtin_nontemporal_load((const u32x4 *)g.y + base + c), v[i]);
-        if constexpr (RES32) {
-            const u32x4 a = __builtin_nontemporal_load((const u32x4 *)g.resid + 2 * (base + c));
-            const u32x4 b = __builtin_nontemporal_load((const u32x4 *)g.resid + 2 * (base + c) + 1);
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                r[i][e] = __uint_as_float(a[e]);
-                r[i][4 + e] = __uint_as_float(b[e]);
-            }
+        const int c = min(tid + T * i, g.nch - 1);
+        if constexpr (WIRE) {
+            const u32x2 q = __builtin_nontemporal_load((const u32x2 *)g.y + base + c);
+            yw[i] = (u32x4){q[0], q[1], 0u, 0u};
         } else {
-            widen(__builtin_nontemporal_load((const u32x4 *)g.resid + base + c), r[i]);
+            yw[i] = __builtin_nontemporal_load((const u32x4 *)g.y + base + c);
+        }
+        if constexpr (RES32) {
+            ra[i] = __builtin_nontemporal_load((const u32x4 *)g.resid + 2 * (base + c));
+            rb[i] = __builtin_nontemporal_load((const u32x4 *)g.resid + 2 * (base + c) + 1);
+        } else {
+            ra[i] = __builtin_nontemporal_load((const u32x4 *)g.resid + base + c);
         }
     }
-    if constexpr (WIRE) {
-        const float s = g.y_scale[row];
+    const float ys = WIRE ? g.y_scale[row] : 1.0f;
 #pragma unroll
-        for (int i = 0; i < CPT; i++)
-#pragma unroll
-            for (int e = 0; e < 8; e++) v[i][e] *= s;
+    for (int i = 0; i < CPT; i++) {
+        const int c = min(tid + T * i, g.nch - 1);
+        pw[i] = g.post_w ? ((const u32x4 *)g.post_w)[c] : ones;
+        gw[i] = g.gate ? *((const u32x4 *)(g.gate + row * g.gate_row) + c) : ones;
+        ww[i] = g.pre_w ? ((const u32x4 *)g.pre_w)[c] : ones;
     }
+
+    float v[CPT][8];
     float mul = g.beta;
-    if (g.post_w) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < CPT; i++)
-#pragma unroll
-            for (int e = 0; e < 8; e++) ss += v[i][e] * v[i][e];
-        mul *= 1.0f / sqrtf(row_sum<T>(ss, red[0]) * inv_n + g.eps);
-    }
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
-        const int c = tid + T * i;
-        if (c >= g.nch) continue;
-        if (g.post_w) {
-            float w[8];
-            widen(((const u32x4 *)g.post_w)[c], w);
+        if constexpr (WIRE) decode((u32x2){yw[i][0], yw[i][1]}, v[i]);
+        else widen(yw[i], v[i]);
+        const float live = tid + T * i < g.nch ? 1.f : 0.f;
+        float sq = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; e++) v[i][e] *= w[e];
+        for (int e = 0; e < 8; e++) {
+            if (WIRE) v[i][e] *= ys;
+            sq += v[i][e] * v[i][e];
         }
-        if (g.gate) {
-            float w[8];
-            widen(*((const u32x4 *)(g.gate + row * g.gate_row) + c), w);
+        ss += live != 0.f ? sq : 0.f;
+    }
+    if (g.post_w) mul *= 1.0f / sqrtf(row_sum<WAVE>(ss, red[0]) * inv_n + g.eps);
+    ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; e++) v[i][e] *= w[e];
+    for (int i = 0; i < CPT; i++) {
+        const int c = tid + T * i;
+        float p[8], q[8], r[8], sq = 0.f;
+        widen(pw[i], p);
+        widen(gw[i], q);
+        if constexpr (RES32) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                r[e] = __uint_as_float(ra[i][e]);
+                r[4 + e] = __uint_as_float(rb[i][e]);
+            }
+        } else {
+            widen(ra[i], r);
         }
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            v[i][e] = g.alpha * r[i][e] + mul * v[i][e];
-            ss += v[i][e] * v[i][e];
+            v[i][e] = g.alpha * r[e] + mul * (v[i][e] * p[e] * q[e]);
+            sq += v[i][e] * v[i][e];
         }
+        if (c >= g.nch) continue;
+        ss += sq;
         if constexpr (RES32) {
             u32x4 a, b;
 #pragma unroll
@@ -162,15 +174,13 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) resnorm_kernel(ResnormArgs 
         }
     }
     if (QB == 0 && !g.z) return;
-    const float rs = 1.0f / sqrtf(row_sum<T>(ss, red[1]) * inv_n + g.eps);
+    const float rs = 1.0f / sqrtf(row_sum<WAVE>(ss, red[1]) * inv_n + g.eps);
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
         const int c = tid + T * i;
         if (c >= g.nch) continue;   // whole scale blocks: N is a multiple of QB
         float w[8], amax = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; e++) w[e] = 1.f;
-        if (g.pre_w) widen(((const u32x4 *)g.pre_w)[c], w);
+        widen(ww[i], w);
 #pragma unroll
         for (int e = 0; e < 8; e++) {
             v[i][e] *= rs * w[e];
@@ -180,13 +190,22 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) resnorm_kernel(ResnormArgs 
         if constexpr (QB == 128) {
             const float s = group_max<16>(amax) / 448.0f;
             if ((c & 15) == 0) ((float *)g.q_scale)[(base + c) >> 4] = s;
-            const double R = s != 0.0f ? 1.0 / (double)s : 0.0;
-            u32x2 o;
+            u32x2 o = {0u, 0u};
+            if (s >= 0x1p-126f) {
+                // z * (1/s): z is itself rounded, so a quotient exact to the last bit
+                // would say no more; |z| / s stays below 448.0002
+                const float inv = 1.0f / s;
 #pragma unroll
-            for (int e = 0; e < 2; e++)
-                o[e] = pack_e4m3x4_sat(wire_quotient(v[i][4 * e], R), wire_quotient(v[i][4 * e + 1], R),
-                                       wire_quotient(v[i][4 * e + 2], R), wire_quotient(v[i][4 * e + 3], R));
-            if (s == 0.0f) o = (u32x2){0u, 0u};
+                for (int e = 0; e < 2; e++)
+                    o[e] = pack_e4m3x4(v[i][4 * e] * inv, v[i][4 * e + 1] * inv, v[i][4 * e + 2] * inv,
+                                       v[i][4 * e + 3] * inv);
+            } else if (s != 0.0f) {   // a subnormal scale, whose reciprocal may not exist in fp32
+                const double R = 1.0 / (double)s;
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+                    o[e] = pack_e4m3x4_sat(wire_quotient(v[i][4 * e], R), wire_quotient(v[i][4 * e + 1], R),
+                                           wire_quotient(v[i][4 * e + 2], R), wire_quotient(v[i][4 * e + 3], R));
+            }
             __builtin_nontemporal_store(o, (u32x2 *)g.q + base + c);
         } else if constexpr (QB == 32) {
             // the smallest k with amax <= 448 * 2^k, from amax's IEEE bits
@@ -195,7 +214,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) resnorm_kernel(ResnormArgs 
             const int ef = (int)(bits >> 23);
             int k = (ef - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 7 : 8);
             if (ef == 0 || k < -127) k = -127;
-            if (k > 120) k = 120;   // an infinite or NaN amax
+            if (k > 120) k = 120;   // an infinite amax
             if ((c & 3) == 0) ((uint8_t *)g.q_scale)[(base + c) >> 2] = m == 0.0f ? 0 : (uint8_t)(k + 127);
             const float inv = __uint_as_float((uint32_t)(127 - k) << 23);   // 2^-k
             u32x2 o;
@@ -209,30 +228,31 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) resnorm_kernel(ResnormArgs 
     }
 }
 
-template <int T, int CPT, bool WIRE, bool RES32>
+template <int CPT, bool WAVE, bool WIRE, bool RES32>
 int launch_q(const ResnormArgs &g, int q_block, dim3 grid, dim3 block, hipStream_t stream) {
-    if (q_block == 128) return bs_enqueue(resnorm_kernel<T, CPT, WIRE, RES32, 128>, grid, block, stream, g);
-    if (q_block == 32) return bs_enqueue(resnorm_kernel<T, CPT, WIRE, RES32, 32>, grid, block, stream, g);
-    return bs_enqueue(resnorm_kernel<T, CPT, WIRE, RES32, 0>, grid, block, stream, g);
+    if (q_block == 128) return bs_enqueue(resnorm_kernel<CPT, WAVE, WIRE, RES32, 128>, grid, block, stream, g);
+    if (q_block == 32) return bs_enqueue(resnorm_kernel<CPT, WAVE, WIRE, RES32, 32>, grid, block, stream, g);
+    return bs_enqueue(resnorm_kernel<CPT, WAVE, WIRE, RES32, 0>, grid, block, stream, g);
 }
 
-template <int T, int CPT>
+template <int CPT, bool WAVE>
 int launch_t(const ResnormArgs &g, bool resid_f32, int q_block, hipStream_t stream) {
-    constexpr int ROWS = T < 256 ? 256 / T : 1;
-    const dim3 grid((unsigned)((g.rows + ROWS - 1) / ROWS)), block(T < 256 ? 256 : T);
+    const dim3 grid((unsigned)(WAVE ? (g.rows + 3) / 4 : g.rows));
+    const dim3 block(WAVE ? 256 : (g.nch + 64 * CPT - 1) / (64 * CPT) * 64);
     if (g.y_scale)
-        return resid_f32 ? launch_q<T, CPT, true, true>(g, q_block, grid, block, stream)
-                         : launch_q<T, CPT, true, false>(g, q_block, grid, block, stream);
-    return resid_f32 ? launch_q<T, CPT, false, true>(g, q_block, grid, block, stream)
-                     : launch_q<T, CPT, false, false>(g, q_block, grid, block, stream);
+        return resid_f32 ? launch_q<CPT, WAVE, true, true>(g, q_block, grid, block, stream)
+                         : launch_q<CPT, WAVE, true, false>(g, q_block, grid, block, stream);
+    return resid_f32 ? launch_q<CPT, WAVE, false, true>(g, q_block, grid, block, stream)
+                     : launch_q<CPT, WAVE, false, false>(g, q_block, grid, block, stream);
 }
 
 }  // namespace
 
 int bs_launch_resnorm(const ResnormArgs &g, bool resid_f32, int q_block, hipStream_t stream) {
     if (g.rows > 0x7FFFFFFF) return -1;
-    if (g.nch <= 128) return launch_t<64, 2>(g, resid_f32, q_block, stream);
-    if (g.nch <= 512) return launch_t<256, 2>(g, resid_f32, q_block, stream);
-    if (g.nch <= 1024) return launch_t<256, 4>(g, resid_f32, q_block, stream);
-    return launch_t<512, 4>(g, resid_f32, q_block, stream);
+    // a row has as few lanes as hold it in CPT packs each, so that few are idle
+    // (N = 7168: 7 waves with 2 packs)
+    if (g.nch <= 128) return launch_t<2, true>(g, resid_f32, q_block, stream);
+    if (g.nch <= 1024) return launch_t<2, false>(g, resid_f32, q_block, stream);
+    return launch_t<4, false>(g, resid_f32, q_block, stream);
 }
