@@ -137,19 +137,6 @@ __device__ __forceinline__ int brow_of(int R) {
     return (R & ~63) + 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3);
 }
 
-// Every descriptor here is workgroup-uniform; readfirstlane says so to the
-// compiler, which otherwise may keep one in VGPRs and wrap each load through
-// it in a loop over distinct values.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, int64_t bytes) {
-    int32_t n = bytes > 0x7FFFFFFFll ? 0x7FFFFFFF : (bytes > 0 ? (int32_t)bytes : 0);
-    const uint64_t b = (uint64_t)base;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
-    n = __builtin_amdgcn_readfirstlane(n);
-    return __builtin_amdgcn_make_buffer_rsrc((void *)(((uint64_t)hi << 32) | lo), (short)0, n,
-                                             0x00020000);
-}
-
 // A tile's operand descriptors: its row panels of A and B, and its scales.
 struct Panels {
     __amdgpu_buffer_rsrc_t rA, rB, rS;   // rS: a_scale (waves 0..3) or b_scale (4..7)
@@ -929,7 +916,8 @@ __device__ __forceinline__ LoraTouch lora_touch(const GemmArgs &g, const LoraGem
     const int64_t m = min(m0 + (tid >> 1), g.M - 1);
     const int half = (tid & 1) * (q.lora.R / 2);
     LoraTouch t;
-    t.b = *(const uint32_t *)(lora_brow(q.lora, a, n0 + (tid >> 1), g.N) + half);
+    const int64_t n = min(n0 + (tid >> 1), g.N - 1);
+    t.b = *(const uint32_t *)(q.lora.B + ((int64_t)a * g.N + n) * q.lora.R + half);
     t.h = __float_as_uint(q.lora.H[m * q.lora.R + half]);
     return t;
 }
@@ -951,7 +939,7 @@ __device__ __forceinline__ void lora_dma(const GemmArgs &g, const LoraGemmArgs &
             const int r = rc + 32 * h + 4 * ((lane & 7) ^ (lane >> 4) ^ (4 * (i & 1)));
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rH, (lds_void *)((h ? stB<ST>() : stA<ST>()) + wave * 4096 + i * 1024), 16,
-                r < R ? (row * R + r) * 4 : 0x7FFFFFF0, 0, 0, 0);
+                r < R ? (row * R + r) * 4 : OUT_OF_RANGE, 0, 0, 0);
         }
     }
 }
@@ -980,17 +968,14 @@ struct LoraWave {
 };
 
 // Half h of ranks rc .. rc+63 of adapter a's B, for the wave's columns from n on;
-// past R, and past N, the offset is out of the descriptor's range and reads as zero.
+// zero past R and N.
 __device__ __forceinline__ void lora_b(v8bf (&b)[TN], const GemmArgs &g, const LoraGemmArgs &q, int a, int64_t n,
                                        int rc, int h, int lane) {
     const int R = q.lora.R, r = rc + 32 * h + 8 * (lane >> 4);
     if (rc + 32 * h >= R) return;
-    const __amdgpu_buffer_rsrc_t rB =
-        make_rsrc(q.lora.B + ((int64_t)a * g.N + n) * R, (g.N - n < WN ? g.N - n : WN) * R * 2);
+    const __amdgpu_buffer_rsrc_t rB = lora_rsrc(q.lora, a, n, g.N);
 #pragma unroll
-    for (int j = 0; j < TN; j++)
-        b[j] = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(
-                                            rB, r < R ? (lora_col(j, lane & 15) * R + r) * 2 : 0x7FFFFFF0, 0, 0));
+    for (int j = 0; j < TN; j++) b[j] = lora_load_b(rB, lora_col(j, lane & 15), r, R);
 }
 
 __device__ __forceinline__ int lora_first(const int (&id)[2], const uint64_t (&todo)[2]) {

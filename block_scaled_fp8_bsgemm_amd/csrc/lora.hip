@@ -169,24 +169,30 @@ __device__ __forceinline__ v8bf load_k(const uint16_t *row, int64_t k, int64_t K
     return __builtin_bit_cast(v8bf, TAIL && k >= K ? z : v);
 }
 
-template <int RT, int CT, bool TAIL>
-__device__ __forceinline__ void shrink_step(v4f (&acc)[RT][CT], const uint16_t *const (&xr)[RT],
-                                            const uint16_t *const (&ar)[CT], int64_t k, int64_t K) {
-    v8bf xv[RT][2], av[CT][2];
+// UN turns of a wave, `step` apart from k on: every load before the first product.
+template <int RT, int CT, int UN, bool TAIL>
+__device__ __forceinline__ void shrink_steps(v4f (&acc)[RT][CT], const uint16_t *const (&xr)[RT],
+                                             const uint16_t *const (&ar)[CT], int64_t k, int64_t step, int64_t K) {
+    v8bf xv[UN][RT][2], av[UN][CT][2];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
+    for (int u = 0; u < UN; u++)
 #pragma unroll
-        for (int i = 0; i < RT; i++) xv[i][h] = load_k<TAIL>(xr[i], k + 8 * h, K);
+        for (int h = 0; h < 2; h++) {
 #pragma unroll
-        for (int j = 0; j < CT; j++) av[j][h] = load_k<TAIL>(ar[j], k + 8 * h, K);
-    }
+            for (int i = 0; i < RT; i++) xv[u][i][h] = load_k<TAIL>(xr[i], k + u * step + 32 * h, K);
 #pragma unroll
-    for (int h = 0; h < 2; h++)
+            for (int j = 0; j < CT; j++) av[u][j][h] = load_k<TAIL>(ar[j], k + u * step + 32 * h, K);
+        }
+    __builtin_amdgcn_sched_barrier(0);   // the loads stay ahead of the products
 #pragma unroll
-        for (int i = 0; i < RT; i++)
+    for (int u = 0; u < UN; u++)
 #pragma unroll
-            for (int j = 0; j < CT; j++)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[j][h], xv[i][h], acc[i][j], 0, 0, 0);
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int i = 0; i < RT; i++)
+#pragma unroll
+                for (int j = 0; j < CT; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[u][j][h], xv[u][i][h], acc[i][j], 0, 0, 0);
 }
 
 // One workgroup: 16 RT rows of one adapter, 16 CT columns of H.  Its W waves
@@ -198,7 +204,7 @@ __device__ __forceinline__ void shrink_step(v4f (&acc)[RT][CT], const uint16_t *
 // row's four lanes so read 128 consecutive bytes.  The adapter's rows are the
 // MFMA's first operand, which leaves a lane four consecutive columns of one
 // row of H.
-template <int RT, int CT, int W>
+template <int RT, int CT, int W, int UN>
 __global__ void __launch_bounds__(W * 64) lora_shrink_kernel(ShrinkArgs g) {
     __shared__ v4f part[W][RT * CT][64];
     const int lane = threadIdx.x & 63;
@@ -224,9 +230,10 @@ __global__ void __launch_bounds__(W * 64) lora_shrink_kernel(ShrinkArgs g) {
         for (int i = 0; i < RT; i++)
 #pragma unroll
             for (int j = 0; j < CT; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-        int64_t k0 = wave * 64;
-        for (; k0 + 64 <= g.K; k0 += W * 64) shrink_step<RT, CT, false>(acc, xr, ar, k0 + 16 * fg, g.K);
-        if (k0 < g.K) shrink_step<RT, CT, true>(acc, xr, ar, k0 + 16 * fg, g.K);
+        int64_t k = wave * 64;
+        for (; k + (UN - 1) * W * 64 + 64 <= g.K; k += UN * W * 64)
+            shrink_steps<RT, CT, UN, false>(acc, xr, ar, k + 8 * fg, W * 64, g.K);
+        for (; k < g.K; k += W * 64) shrink_steps<RT, CT, 1, true>(acc, xr, ar, k + 8 * fg, 0, g.K);
 #pragma unroll
         for (int i = 0; i < RT; i++)
 #pragma unroll
@@ -320,10 +327,12 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(ExpandArgs g) {
     const int64_t first = (int64_t)((int)blockIdx.x - tile * g.col_blocks) * g.chunks;
     const int64_t end = min((first + g.chunks) * 256, g.N);
     const int dx = 8 * fg + (up ? 32 : 0), dy = 8 * fg + (up ? 0 : 32);
+    const int64_t c0 = first * 256;
+    const __amdgpu_buffer_rsrc_t rB = lora_rsrc(g.lora, has ? t.group : 0, c0, g.N);
     auto load_b = [&](v8bf(&b)[4], int64_t n, int r0) {
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            b[j] = lora_load_b(lora_brow(g.lora, t.group, n + lora_col(j, fr), g.N), r0 + 8 * fg, g.lora.R);
+            b[j] = lora_load_b(rB, (int)(n - c0) + lora_col(j, fr), r0 + 8 * fg, g.lora.R);
     };
     v8bf bnext[4];
     if (has) load_b(bnext, first * 256 + wave * 64, 0);
@@ -397,15 +406,26 @@ int bs_launch_lora_plan(const int32_t *ids, int32_t *plan, int64_t M, int L, hip
     return bs_enqueue(lora_plan_kernel, dim3(L + 1), dim3(PLAN_WAVES * 64), stream, ids, plan, M, L);
 }
 
+template <int RT, int CT, int UN>
+static int launch_shrink(const ShrinkArgs &g, hipStream_t stream) {
+    constexpr int W = 8;
+    const dim3 grid((unsigned)max_tiles(g.M, g.L, 16 * RT), (unsigned)((g.R + 16 * CT - 1) / (16 * CT)));
+    return bs_enqueue(lora_shrink_kernel<RT, CT, W, UN>, grid, dim3(64 * W), stream, g);
+}
+
+// Long batches take 64 rows and 64 ranks a workgroup, which reads x once and A
+// once per 64 rows; shorter ones spread the ranks over workgroups, since one CU
+// then waits for fewer of A's bytes.  Graph launches at K = 2048, R = 64, 8
+// adapters, us for (64 rows, 64 ranks) / (16, 64) / (16, 32) / (16, 16): M = 16384:
+// 20.4 / 37.6 / 44.6 / 56.3; M = 4096: 18.5 / 12.8 / 14.5 / 19.6; M = 1024: 18.0 /
+// 12.5 / 9.0 / 10.9; M = 256, mixed: 15.4 / 11.7 / 8.5 / 6.8.
 int bs_launch_lora_shrink(const uint16_t *x, const uint16_t *A, const int32_t *plan, float *H, int64_t M, int64_t K,
                           int L, int R, hipStream_t stream) {
     const ShrinkArgs g = {x, A, plan, H, (int)M, L, R, K};
-    if (M >= 64 * (int64_t)(L + 1)) {
-        const dim3 grid((unsigned)max_tiles(M, L, 32), (unsigned)((R + 63) / 64));
-        return bs_enqueue(lora_shrink_kernel<2, 4, 4>, grid, dim3(256), stream, g);
-    }
-    const dim3 grid((unsigned)max_tiles(M, L, 16), (unsigned)((R + 63) / 64));
-    return bs_enqueue(lora_shrink_kernel<1, 4, 8>, grid, dim3(512), stream, g);
+    if (M >= 8192) return launch_shrink<4, 4, 1>(g, stream);
+    if (M >= 2048) return launch_shrink<1, 4, 2>(g, stream);
+    if (M >= 512) return launch_shrink<1, 2, 2>(g, stream);
+    return launch_shrink<1, 1, 4>(g, stream);
 }
 
 template <int RT, int RMAX>
@@ -419,6 +439,7 @@ static int launch_expand(ExpandArgs g, hipStream_t stream) {
     // 97.4 / 117.8 at one chunk to each.
     int64_t chunks = tiles * cols / 1024;
     chunks = chunks < 1 ? 1 : chunks > cols ? cols : chunks;
+    if (chunks > 4096) chunks = 4096;   // offsets within a workgroup's part of B: below 2^30
     g.chunks = (int)chunks;
     g.col_blocks = (int)((cols + chunks - 1) / chunks);
     if (tiles * g.col_blocks > 0x7FFFFFFF) return -1;
