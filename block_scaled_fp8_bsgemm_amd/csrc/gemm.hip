@@ -1523,6 +1523,158 @@ __global__ void __launch_bounds__(NTHREADS) bsgemm_pb_tile_kernel(GemmArgs g) { 
 
 __global__ void __launch_bounds__(NTHREADS) mxgemm_tile_kernel(GemmArgs g) { gemm_tile<MODE_MX>(g); }
 
+// ---- few rows, with adapters -------------------------------------------------
+// The 256-row tile leaves a short batch on N / 256 of the CUs, waiting for B.
+// Here a wave takes 16 RG rows x 16 CG columns by itself, straight from global
+// memory to registers, D K blocks ahead, one wave to a workgroup (two or four
+// side by side took 1.3 to 2.5 times as long: they wait on one CU).  Each K block is the same MFMA on the same fragments, folded in the same order, so the
+// sums are those of the other kernels bit for bit.  The 16-column sub-tiles take B's
+// rows in the order of lora_col, two sub-tiles to a 16-byte piece of C.
+template <int RG, int CG>
+struct ShortBlock {
+    v8i a[RG], b[CG];
+    float sa[RG], sb;
+};
+
+__device__ __forceinline__ v8i frag_of(__amdgpu_buffer_rsrc_t r, int off, int k) {
+    const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(r, off, k, 0);
+    const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(r, off + 64, k, 0);
+    return (v8i){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+template <int RG, int CG, int D>
+__global__ void __launch_bounds__(64) bsgemm_lora_short_kernel(GemmArgs g, LoraGemmArgs q) {
+    const int lane = threadIdx.x;
+    const int frow = lane & 15, fg = lane >> 4;
+    // workgroups are dealt to the XCDs in turn: the row tiles of one column block
+    // follow each other on one XCD, whose L2 then serves B to all but the first
+    const int tm = (int)((g.M + 16 * RG - 1) / (16 * RG));
+    const int turn = blockIdx.x / NUM_XCD;
+    const int cb = turn / tm * NUM_XCD + (int)(blockIdx.x % NUM_XCD);
+    const int64_t m0 = (int64_t)(turn % tm) * (16 * RG);
+    const int64_t n = (int64_t)cb * (16 * CG);
+    if (n >= g.N) return;
+    const int rows_in = (int)(g.M - m0 < 16 * RG ? g.M - m0 : 16 * RG);
+    const int K = (int)g.K, KB = g.KB;
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.A + m0 * K, (int64_t)rows_in * K);
+    const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.B + n * K, (int64_t)(16 * CG) * K);
+    const __amdgpu_buffer_rsrc_t rS = make_rsrc((const float *)g.sa + m0 * KB, (int64_t)rows_in * KB * 4);
+    const float *sb = (const float *)g.sb + n / 128 * KB;
+    const int offA = frow * K + 16 * fg;
+    int offB[CG];
+#pragma unroll
+    for (int j = 0; j < CG; j++) offB[j] = lora_col(j, frow) * K + 16 * fg;
+
+    // a block past the last one loads that again, and is not used
+    auto load = [&](ShortBlock<RG, CG> &x, int kb) {
+        kb = min(kb, KB - 1);
+#pragma unroll
+        for (int j = 0; j < CG; j++) x.b[j] = frag_of(rB, offB[j], kb * 128);
+#pragma unroll
+        for (int i = 0; i < RG; i++) x.a[i] = frag_of(rA, offA + i * 16 * K, kb * 128);
+#pragma unroll
+        for (int i = 0; i < RG; i++)
+            x.sa[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rS, (16 * i + frow) * KB * 4, kb * 4, 0));
+        x.sb = sb[kb];
+    };
+    v4f acc[RG][CG];
+#pragma unroll
+    for (int i = 0; i < RG; i++)
+#pragma unroll
+        for (int j = 0; j < CG; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+    ShortBlock<RG, CG> x[D];
+#pragma unroll
+    for (int d = 0; d < D; d++) load(x[d], d);
+    for (int kb = 0; kb < KB; kb += D) {
+#pragma unroll
+        for (int d = 0; d < D; d++) {
+            if (kb + d >= KB) break;
+            v4f p[RG][CG];
+#pragma unroll
+            for (int i = 0; i < RG; i++)
+#pragma unroll
+                for (int j = 0; j < CG; j++)
+                    p[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        x[d].b[j], x[d].a[i], (v4f){0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < RG; i++) {
+                const float s = x[d].sa[i] * x[d].sb;
+#pragma unroll
+                for (int j = 0; j < CG; j++) fold4(acc[i][j], p[i][j], s);
+            }
+            load(x[d], kb + d + D);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // The adapters, four at a time, so that a batch of single tokens does not wait
+    // for each one's B in turn; H of the wave's rows is loaded and split once per 32 ranks.
+    const int R = q.lora.R;
+    int id = -1;
+    if (lane < rows_in) id = q.ids[m0 + lane];
+    if ((uint32_t)id >= (uint32_t)q.lora.L) id = -1;
+    const uint64_t all = __ballot(id >= 0);
+    if (all) {
+        float s[RG];
+        int idr[RG];
+#pragma unroll
+        for (int i = 0; i < RG; i++) {
+            idr[i] = __shfl(id, 16 * i + frow, 64);
+            s[i] = q.lora.scale ? q.lora.scale[max(idr[i], 0)] : 1.0f;
+        }
+        for (int r0 = 0; r0 < R; r0 += 32) {
+            const int r = r0 + 8 * fg;
+            v8bf hi[RG], lo[RG];
+#pragma unroll
+            for (int i = 0; i < RG; i++)
+                lora_split(lora_load_h(q.lora, m0 + 16 * i + frow, idr[i] >= 0, r), s[i], hi[i], lo[i]);
+            uint64_t todo = all;
+            while (todo) {
+                int a[4];
+                v8bf b[4][CG];
+#pragma unroll
+                for (int t = 0; t < 4; t++) {
+                    a[t] = -2;   // no row's
+                    if (!todo) continue;
+                    a[t] = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)todo) - 1);
+                    todo &= ~__ballot(id == a[t]);
+                    const __amdgpu_buffer_rsrc_t rL = lora_rsrc(q.lora, a[t], n, g.N);
+#pragma unroll
+                    for (int j = 0; j < CG; j++) b[t][j] = lora_load_b(rL, lora_col(j, frow), r, R);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; t++) {
+                    if (a[t] < 0) continue;
+#pragma unroll
+                    for (int i = 0; i < RG; i++) {
+                        const u32x4 z = {0u, 0u, 0u, 0u};
+                        const v8bf h = __builtin_bit_cast(v8bf, idr[i] == a[t] ? __builtin_bit_cast(u32x4, hi[i]) : z);
+                        const v8bf l = __builtin_bit_cast(v8bf, idr[i] == a[t] ? __builtin_bit_cast(u32x4, lo[i]) : z);
+#pragma unroll
+                        for (int j = 0; j < CG; j++) {
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], h, acc[i][j], 0, 0, 0);
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], l, acc[i][j], 0, 0, 0);
+                        }
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RG; i++) {
+        if (16 * i + frow >= rows_in) continue;
+        const uint32_t m = (uint32_t)(m0 + 16 * i + frow), br = (uint32_t)g.band_rows, d = m / br;
+        uint16_t *row = g.C + (int64_t)d * g.band_stride + (int64_t)(m - d * br) * g.N + n + 8 * fg;
+#pragma unroll
+        for (int j = 0; j < CG; j += 2) {
+            const u32x4 o = {pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]),
+                             pack_bf16x2(acc[i][j + 1][0], acc[i][j + 1][1]),
+                             pack_bf16x2(acc[i][j + 1][2], acc[i][j + 1][3])};
+            *(u32x4 *)(row + 16 * j) = o;
+        }
+    }
+}
+
 // B [N, K] -> the prepacked layout [N/16][K/128][2][64][16 B]: unit u of the
 // output (16 bytes) is half h, lane l = 16 g + r of 16-row group nt and K
 // block kb, and holds bytes [16 g + 64 h, +16) of row brow_of(16 nt + r)'s K
@@ -1609,6 +1761,20 @@ int bs_launch_gemm_lora(const uint8_t *A, const float *sa, const uint8_t *B, con
                         int64_t band_stride, hipStream_t stream) {
     const GemmArgs g = gemm_args(A, sa, B, sb, C, M, N, K, band_rows, band_stride);
     const LoraGemmArgs q = {lora, ids};
+    // Short batches by waves of 16 x 32, 32 x 64 or 64 x 64, whichever is the first to
+    // need at most 512 of them (two to a CU): a smaller wave tile waits less, a
+    // larger one reads less.  K = 2048, R = 16, us by graph launches, for the three
+    // and the 256-row tile: N = 7168, M = 16: 9.0 / 12.8 / 19.2 / 27.0; M = 64: 19.3 /
+    // 13.9 / 21.2 / 28.5; M = 256: 58 / 34 / 26 / 34; M = 384: 96 / 49 / 36 / 34;
+    // N = 1024, M = 256: 11.1 / 12.4 / 19.4 / 31.0; M = 1024: 35 / 19.5 / 22 / 33.
+    const auto waves = [&](int rows, int cols) { return N / cols * ((M + rows - 1) / rows); };
+    const auto run_short = [&](auto kernel, int rows, int cols) {
+        const int64_t blocks = (N / cols + NUM_XCD - 1) / NUM_XCD * NUM_XCD * ((M + rows - 1) / rows);
+        return bs_enqueue(kernel, dim3((unsigned)blocks), dim3(64), stream, g, q);
+    };
+    if (waves(16, 32) <= 512) return run_short(bsgemm_lora_short_kernel<1, 2, 4>, 16, 32);
+    if (waves(32, 64) <= 512) return run_short(bsgemm_lora_short_kernel<2, 4, 3>, 32, 64);
+    if (waves(64, 64) <= 512) return run_short(bsgemm_lora_short_kernel<4, 4, 2>, 64, 64);
     return bs_enqueue(bsgemm_lora_tile_kernel, dim3(gemm_grid(g)), dim3(NTHREADS), stream, g, q);
 }
 

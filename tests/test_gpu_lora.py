@@ -254,8 +254,11 @@ def run_gemm(ops, H, B, ids, scale, bands, stride, L):
     return C[to_dev(at.reshape(-1))].view(M, N)
 
 
-GEMM = [(1, 128, 128, 1, 8, 1, 0), (16, 128, 256, 3, 16, 1, 0), (200, 384, 256, 4, 16, 4, 50 * 384 + 64),
+GEMM = [(1, 128, 128, 1, 8, 1, 0), (1, 7168, 2048, 16, 16, 1, 0), (15, 384, 640, 20, 40, 5, 3 * 384 + 8),
+        (17, 256, 896, 2, 64, 1, 0), (33, 1152, 512, 40, 24, 3, 0), (64, 640, 384, 64, 72, 8, 0),
+        (65, 512, 256, 3, 128, 13, 5 * 512 + 16), (256, 768, 1024, 5, 16, 2, 0), (257, 768, 1024, 5, 16, 1, 0), (16, 128, 256, 3, 16, 1, 0), (200, 384, 256, 4, 16, 4, 50 * 384 + 64),
         (300, 640, 384, 70, 64, 3, 0), (513, 512, 1152, 5, 128, 1, 0), (1040, 1280, 512, 2, 40, 8, 0),
+        (520, 1024, 384, 3, 48, 4, 0), (2050, 2304, 128, 3, 16, 1, 0), (2100, 2304, 384, 4, 72, 7, 0),
         (2600, 5120, 256, 6, 24, 8, 0), (2056, 2304, 512, 9, 256, 8, 257 * 2304 + 8)]
 
 
@@ -280,7 +283,8 @@ def test_gemm_exact_integers(M, N, K, L, R, bands, stride):
         assert torch.equal(got[none].float(), plain[none].float())
 
 
-@pytest.mark.parametrize("M,N,K,L,R", [(200, 512, 256, 4, 16), (700, 1024, 640, 3, 64), (1300, 1280, 512, 8, 32)])
+@pytest.mark.parametrize("M,N,K,L,R", [(5, 384, 1152, 4, 48), (200, 512, 256, 4, 16), (700, 1024, 640, 3, 64), (1300, 1280, 512, 8, 32),
+                                         (2300, 2304, 640, 3, 136)])
 def test_gemm_random(M, N, K, L, R):
     """Inside the fp8 product's interval, widened by the low-rank product's bound and
     2R fp32 additions onto the accumulator."""
