@@ -878,6 +878,7 @@ struct LoraGemmArgs {
 
 // ids of the tile's rows, loaded with the tile's first K block
 __shared__ int32_t sI[BM];
+__shared__ float sR[BM];   // and their adapters' scales, before the last K block
 
 // Waves 0..3 take 64 each; rows past M read as 0 and are told apart by their number.
 __device__ __forceinline__ void load_ids(const GemmArgs &g, const LoraGemmArgs &q, int64_t m0, int wave, int lane) {
@@ -897,29 +898,6 @@ __device__ __forceinline__ bool tile_has_adapter(const GemmArgs &g, const LoraGe
 #pragma unroll
     for (int h = 0; h < 4; h++) has |= id_of(g, q, m0, 64 * h + lane) >= 0;
     return __ballot(has) != 0;
-}
-
-// Brings the tile's rows of H, and of B of its first adapter, into L2 while the
-// K loop runs: a lane reads one word of half a row of each and drops it.
-struct LoraTouch {
-    uint32_t b, h;
-};
-__device__ __forceinline__ LoraTouch lora_touch(const GemmArgs &g, const LoraGemmArgs &q, int64_t m0, int64_t n0,
-                                                int tid, int lane) {
-    int a = -1;
-#pragma unroll
-    for (int h = 0; h < 4; h++) {
-        const int id = id_of(g, q, m0, 64 * h + lane);
-        const uint64_t has = __ballot(id >= 0);
-        if (a < 0 && has) a = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)has) - 1);
-    }
-    const int64_t m = min(m0 + (tid >> 1), g.M - 1);
-    const int half = (tid & 1) * (q.lora.R / 2);
-    LoraTouch t;
-    const int64_t n = min(n0 + (tid >> 1), g.N - 1);
-    t.b = *(const uint32_t *)(q.lora.B + ((int64_t)a * g.N + n) * q.lora.R + half);
-    t.h = __float_as_uint(q.lora.H[m * q.lora.R + half]);
-    return t;
 }
 
 // H's ranks rc .. rc+63 into stage ST: slot i of wave w as in load_stage; a chunk
@@ -1058,8 +1036,7 @@ __device__ __forceinline__ void lora_add(v4f (&acc)[TM][TN], const GemmArgs &g, 
     LoraWave w;
     lora_begin(w, g, q, m0, n, wm, lane);
     const int R = q.lora.R;
-    float cs = 1.0f;   // the scale of the row this lane splits
-    if (q.lora.scale) cs = q.lora.scale[max(id_of(g, q, m0, wave * 32 + (lane & 31)), 0)];
+    const float cs = sR[wave * 32 + (lane & 31)];   // the scale of the row this lane splits
     for (int rc = 0;;) {
         if (rc + 64 < R) lora_dma<0>(g, q, m0, rc + 64, wave, lane);
         lora_chunk<1>(acc, w, g, q, cs, n, rc, wm, wave, lane);
@@ -1169,10 +1146,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
         read_head<1>(a, bf, s, wm, wn, frow, fc);
     }
 
-    LoraTouch touch = {0u, 0u};
+    float scale = 1.0f;   // of tile row tid's adapter, for tid < 256
     if constexpr (LORA) {
         any = tile_has_adapter(g, q, m0, lane);
-        if (any) touch = lora_touch(g, q, m0, n0, tid, lane);
+        if (any && q.lora.scale) scale = q.lora.scale[max(id_of(g, q, m0, tid & (BM - 1)), 0)];
     }
     // nothing pending before the first block: its first three folds add 0 * 0
     v4f p[4];
@@ -1190,7 +1167,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
         kblock<0>(acc, p, s_tail, a, bf, s, L, L.P, kb + 2, kb + 2 < KB, wm, wn, frow, fc);
     }
     if constexpr (LORA) {
-        asm volatile("" ::"v"(touch.b), "v"(touch.h));
+        if (tid < BM) sR[tid] = scale;
         if (kb < KB) {   // the last two blocks, the second without a successor
             kblock<1>(acc, p, s_tail, a, bf, s, L, L.P, kb + 1, true, wm, wn, frow, fc);
             if (any) lora_dma<1>(g, q, m0, 0, wave, lane);
