@@ -251,8 +251,11 @@ int launch_t(const ResnormArgs &g, bool resid_f32, int q_block, hipStream_t stre
 int bs_launch_resnorm(const ResnormArgs &g, bool resid_f32, int q_block, hipStream_t stream) {
     if (g.rows > 0x7FFFFFFF) return -1;
     // a row has as few lanes as hold it in CPT packs each, so that few are idle
-    // (N = 7168: 7 waves with 2 packs)
+    // (N = 7168: 7 waves of 2 packs, or 4 of 4).  Few rows want the shorter chain
+    // of 2 packs, many the fewer waves to join: graph launches of wire rows to
+    // codes at N = 7168, 2 packs / 4: 1 row 4.8 / 5.5 us, 64 rows 4.6 / 5.4, 16384
+    // rows 130 / 126; 2512 bf16 rows of 1536 to bf16: 10.1 / 8.9.
     if (g.nch <= 128) return launch_t<2, true>(g, resid_f32, q_block, stream);
-    if (g.nch <= 1024) return launch_t<2, false>(g, resid_f32, q_block, stream);
+    if (g.nch <= 1024 && g.rows < 512) return launch_t<2, false>(g, resid_f32, q_block, stream);
     return launch_t<4, false>(g, resid_f32, q_block, stream);
 }
