@@ -401,19 +401,20 @@ def _args(what, stream, *args):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{name} must be a device tensor")
+        if d != dev:
+            if d < 0:
+                raise ValueError(f"{name} must be a device tensor")
+            if dev is not None:
+                raise ValueError(f"{what}: tensors on cuda:{dev} and cuda:{d}")
+            dev = d
         if t.dtype not in dtypes:
             raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"{what}: tensors on cuda:{dev} and cuda:{d}")
         out.append(t.data_ptr())
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{what}: tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    here = torch.cuda.current_device()
+    if dev != here:
+        raise ValueError(f"{what}: tensors on cuda:{dev}, but the current device is cuda:{here}")
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(dev)   # current_stream() alone takes 2.7 us
     elif stream.device.index != dev:
@@ -433,12 +434,25 @@ def _is(t, shape, name):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _fits(t, n, name):
+    if t.numel() < n:
+        raise ValueError(f"{name}: {t.numel()} elements, the call writes {n}")
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    return t.shape
+
+
 def lora_plan(ids, n_adapters, plan=None, stream=None):
     """plan (int32 [n_adapters + 2 + M]) = the rows of ids (int32 [M]) ordered by adapter: group
     starts, then rows (see bsgemm.h); an id outside [0, n_adapters) means no adapter."""
     ty = _ty()
-    _need(ids.dim() == 1, f"ids must be 1-D, got shape {tuple(ids.shape)}")
-    _need(n_adapters >= 1, f"lora_plan: n_adapters must be at least 1, got {n_adapters}")
+    if not (ids.dim() == 1):
+        raise ValueError(f"ids must be 1-D, got shape {tuple(ids.shape)}")
+    if not (n_adapters >= 1):
+        raise ValueError(f"lora_plan: n_adapters must be at least 1, got {n_adapters}")
     M = ids.shape[0]
     if plan is None:
         plan = ty.torch.empty(n_adapters + 2 + M, dtype=ty.torch.int32, device=ids.device)
@@ -452,13 +466,14 @@ def lora_shrink(x, A, plan, H=None, stream=None):
     """H (fp32 [M,R]) = each row of x (bf16 [M,K]) times its adapter's A (bf16 [n_adapters,R,K])
     transposed, by the plan of lora_plan; zero rows where there is no adapter."""
     ty = _ty()
-    M, K = _dims2(x, "x")
-    _need(A.dim() == 3 and A.shape[2] == K, f"A: shape {tuple(A.shape)}, expected [n_adapters, R, {K}]")
+    M, K = _matrix(x, "x")
+    if not (A.dim() == 3 and A.shape[2] == K):
+        raise ValueError(f"A: shape {tuple(A.shape)}, expected [n_adapters, R, {K}]")
     L, R, _ = A.shape
     _check_plan(plan, M, L)
     if H is None:
         H = ty.torch.empty((M, R), dtype=ty.torch.float32, device=x.device)
-    _room(H, M * R, "H")
+    _fits(H, M * R, "H")
     p, st = _args("lora_shrink", stream, (x, ty.bf, "x"), (A, ty.bf, "A"), (plan, ty.i32, "plan"), (H, ty.f32, "H"))
     if M:
         _check(load().lora_shrink(*p, M, K, L, R, st), "lora_shrink")
@@ -466,10 +481,12 @@ def lora_shrink(x, A, plan, H=None, stream=None):
 
 
 def _check_lora(H, B, scale, N, what):
-    M, R = _dims2(H, "H")
-    _need(B.dim() == 3 and B.shape[2] == R, f"{what}: shape {tuple(B.shape)}, expected [n_adapters, N, {R}]")
+    M, R = _matrix(H, "H")
+    if not (B.dim() == 3 and B.shape[2] == R):
+        raise ValueError(f"{what}: shape {tuple(B.shape)}, expected [n_adapters, N, {R}]")
     if N is not None:
-        _need(B.shape[1] == N, f"{what}: shape {tuple(B.shape)}, expected [n_adapters, {N}, {R}]")
+        if not (B.shape[1] == N):
+            raise ValueError(f"{what}: shape {tuple(B.shape)}, expected [n_adapters, {N}, {R}]")
     if scale is not None:
         _is(scale, (B.shape[0],), "scale")
     return M, B.shape[1], B.shape[0], R
@@ -482,10 +499,11 @@ def lora_expand(H, B, plan, base, out=None, scale=None, bands=1, band_stride=0, 
     M, N, L, R = _check_lora(H, B, scale, None, "B")
     _check_plan(plan, M, L)
     need = _band_elems(M, N, bands, band_stride)
-    _need(base.numel() >= need, f"base: {base.numel()} elements, the call reads {need}")
+    if not (base.numel() >= need):
+        raise ValueError(f"base: {base.numel()} elements, the call reads {need}")
     if out is None:
         out = ty.torch.empty(need, dtype=ty.torch.bfloat16, device=base.device)
-    _room(out, need, "out")
+    _fits(out, need, "out")
     p, st = _args("lora_expand", stream, (H, ty.f32, "H"), (B, ty.bf, "B"), (scale, ty.f32, "scale"),
                   (plan, ty.i32, "plan"), (base, ty.bf, "base"), (out, ty.bf, "out"))
     if M:
@@ -500,12 +518,13 @@ def bsgemm_fp8_lora(A, a_scale, B, b_scale, H, lora_B, ids, scale=None, C=None, 
     ty = _ty()
     M, N, K = _check_gemm_operands(A, a_scale, B, b_scale, 128, "bsgemm_fp8_lora")
     Mh, _, L, R = _check_lora(H, lora_B, scale, N, "lora_B")
-    _need(Mh == M, f"H: {Mh} rows, A has {M}")
+    if not (Mh == M):
+        raise ValueError(f"H: {Mh} rows, A has {M}")
     _is(ids, (M,), "ids")
     need = _band_elems(M, N, bands, band_stride)
     if C is None:
         C = ty.torch.empty(need, dtype=ty.torch.bfloat16, device=A.device)
-    _room(C, need, "C")
+    _fits(C, need, "C")
     p, st = _args("bsgemm_fp8_lora", stream, (A, ty.u8, "A"), (a_scale, ty.f32, "a_scale"), (B, ty.u8, "B"),
                   (b_scale, ty.f32, "b_scale"), (H, ty.f32, "H"), (lora_B, ty.bf, "lora_B"), (scale, ty.f32, "scale"),
                   (ids, ty.i32, "ids"), (C, ty.b16, "C"))
@@ -526,9 +545,10 @@ def resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.
     buffer is given, or (quant=0) always; what is not written is returned as None."""
     ty = _ty()
     torch = ty.torch
-    rows, N = _dims2(y, "y")
+    rows, N = _matrix(y, "y")
     _is(resid, (rows, N), "resid")
-    _need(quant in (0, 32, 128), f"resnorm: quant must be 0, 32 or 128, got {quant}")
+    if quant not in (0, 32, 128):
+        raise ValueError(f"resnorm: quant must be 0, 32 or 128, got {quant}")
     if y_scale is not None and y_scale.numel() != rows:
         raise ValueError(f"y_scale: {y_scale.numel()} elements for {rows} rows")
     if post_w is not None:
@@ -543,22 +563,25 @@ def resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.
         resid_out = torch.empty_like(resid)
     elif resid_out.dtype != resid.dtype:
         raise ValueError(f"resid_out is {resid_out.dtype}, resid is {resid.dtype}")
-    _room(resid_out, rows * N, "resid_out")
+    n = rows * N
+    _fits(resid_out, n, "resid_out")
     if quant:
-        _need(N % quant == 0, f"resnorm: N={N} is not a multiple of quant={quant}")
+        if N % quant:
+            raise ValueError(f"resnorm: N={N} is not a multiple of quant={quant}")
         if q is None:
             q = torch.empty((rows, N), dtype=torch.uint8, device=y.device)
         if q_scale is None:
             q_scale = torch.empty((rows, N // quant), dtype=torch.float32 if quant == 128 else torch.uint8,
                                   device=y.device)
-        _room(q, rows * N, "q")
-        _room(q_scale, rows * (N // quant), "q_scale")
+        _fits(q, n, "q")
+        _fits(q_scale, n // quant, "q_scale")
     else:
-        _need(q is None and q_scale is None, "resnorm: q and q_scale need quant=32 or 128")
+        if not (q is None and q_scale is None):
+            raise ValueError("resnorm: q and q_scale need quant=32 or 128")
         if z is None:
             z = torch.empty((rows, N), dtype=torch.bfloat16, device=y.device)
     if z is not None:
-        _room(z, rows * N, "z")
+        _fits(z, n, "z")
     p, st = _args("resnorm", stream, (y, ty.bf if y_scale is None else ty.u8, "y"), (y_scale, ty.f32, "y_scale"),
                   (resid, ty.resid, "resid"), (post_w, ty.bf, "post_w"), (gate, ty.bf, "gate"), (pre_w, ty.bf, "pre_w"),
                   (resid_out, ty.resid, "resid_out"), (z, ty.bf, "z"), (q, ty.u8, "q"),
