@@ -1527,6 +1527,86 @@ __device__ __forceinline__ v8i frag_of(__amdgpu_buffer_rsrc_t r, int off, int k)
     return (v8i){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+// The adapters of a wave's 16 RG rows from m0 on (rows_in of them inside M) and 16 CG
+// columns from n on, added to its finished accumulators: four adapters at a time, so
+// that a batch of single tokens does not wait for each one's B in turn; H of the
+// wave's rows is loaded and split once per 32 ranks.
+template <int RG, int CG>
+__device__ __forceinline__ void wave_adapters(v4f (&acc)[RG][CG], const GemmArgs &g, const LoraGemmArgs &q, int64_t m0,
+                                              int64_t n, int rows_in, int lane) {
+    const int frow = lane & 15, fg = lane >> 4;
+    const int R = q.lora.R;
+    int id = -1;
+    if (lane < rows_in) id = q.ids[m0 + lane];
+    if ((uint32_t)id >= (uint32_t)q.lora.L) id = -1;
+    const uint64_t all = __ballot(id >= 0);
+    if (all) {
+        float s[RG];
+        int idr[RG];
+#pragma unroll
+        for (int i = 0; i < RG; i++) {
+            idr[i] = __shfl(id, 16 * i + frow, 64);
+            s[i] = q.lora.scale ? q.lora.scale[max(idr[i], 0)] : 1.0f;
+        }
+        for (int r0 = 0; r0 < R; r0 += 32) {
+            const int r = r0 + 8 * fg;
+            v8bf hi[RG], lo[RG];
+#pragma unroll
+            for (int i = 0; i < RG; i++)
+                lora_split(lora_load_h(q.lora, m0 + 16 * i + frow, idr[i] >= 0, r), s[i], hi[i], lo[i]);
+            uint64_t todo = all;
+            while (todo) {
+                int a[4];
+                v8bf b[4][CG];
+#pragma unroll
+                for (int t = 0; t < 4; t++) {
+                    a[t] = -2;   // no row's
+                    if (!todo) continue;
+                    a[t] = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)todo) - 1);
+                    todo &= ~__ballot(id == a[t]);
+                    const __amdgpu_buffer_rsrc_t rL = lora_rsrc(q.lora, a[t], n, g.N);
+#pragma unroll
+                    for (int j = 0; j < CG; j++) b[t][j] = lora_load_b(rL, lora_col(j, frow), r, R);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; t++) {
+                    if (a[t] < 0) continue;
+#pragma unroll
+                    for (int i = 0; i < RG; i++) {
+                        const u32x4 z = {0u, 0u, 0u, 0u};
+                        const v8bf h = __builtin_bit_cast(v8bf, idr[i] == a[t] ? __builtin_bit_cast(u32x4, hi[i]) : z);
+                        const v8bf l = __builtin_bit_cast(v8bf, idr[i] == a[t] ? __builtin_bit_cast(u32x4, lo[i]) : z);
+#pragma unroll
+                        for (int j = 0; j < CG; j++) {
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], h, acc[i][j], 0, 0, 0);
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], l, acc[i][j], 0, 0, 0);
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int RG, int CG>
+__device__ __forceinline__ void wave_store(const v4f (&acc)[RG][CG], const GemmArgs &g, int64_t m0, int64_t n,
+                                           int rows_in, int lane) {
+    const int frow = lane & 15, fg = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < RG; i++) {
+        if (16 * i + frow >= rows_in) continue;
+        const uint32_t m = (uint32_t)(m0 + 16 * i + frow), br = (uint32_t)g.band_rows, d = m / br;
+        uint16_t *row = g.C + (int64_t)d * g.band_stride + (int64_t)(m - d * br) * g.N + n + 8 * fg;
+#pragma unroll
+        for (int j = 0; j < CG; j += 2) {
+            const u32x4 o = {pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]),
+                             pack_bf16x2(acc[i][j + 1][0], acc[i][j + 1][1]),
+                             pack_bf16x2(acc[i][j + 1][2], acc[i][j + 1][3])};
+            *(u32x4 *)(row + 16 * j) = o;
+        }
+    }
+}
+
 template <int RG, int CG, int D>
 __global__ void __launch_bounds__(64) bsgemm_lora_short_kernel(GemmArgs g, LoraGemmArgs q) {
     const int lane = threadIdx.x;
@@ -1592,72 +1672,127 @@ __global__ void __launch_bounds__(64) bsgemm_lora_short_kernel(GemmArgs g, LoraG
         }
     }
 
-    // The adapters, four at a time, so that a batch of single tokens does not wait
-    // for each one's B in turn; H of the wave's rows is loaded and split once per 32 ranks.
-    const int R = q.lora.R;
-    int id = -1;
-    if (lane < rows_in) id = q.ids[m0 + lane];
-    if ((uint32_t)id >= (uint32_t)q.lora.L) id = -1;
-    const uint64_t all = __ballot(id >= 0);
-    if (all) {
-        float s[RG];
-        int idr[RG];
+    wave_adapters<RG, CG>(acc, g, q, m0, n, rows_in, lane);
+    wave_store<RG, CG>(acc, g, m0, n, rows_in, lane);
+}
+
+// ---- middling batches, with adapters -----------------------------------------
+// 64 rows x 128 columns to a workgroup of 8 waves (2 x 4, 32 x 32 each), A, B and
+// the row scales staged by DMA three K blocks deep: too few tiles of 256 rows to
+// fill the CUs, too many rows for every wave to load its own fragments.  A stage is
+// one LDS object (so that the compiler can tell the DMA into one from the reads of
+// another): 8 KiB of A and 16 KiB of B in the slots of lds_slot, then each wave's
+// copy of the 64 rows' scales.  Three stages let two workgroups share a CU; four
+// took as long for one workgroup to a CU and 28 against 22 us for two.
+//
+// At K block kb a wave waits until its own DMA of kb has landed (that of the next
+// block may be in flight), meets the others, whose reads of block kb - 1 are then
+// done too, sends block kb + 2 to the stage kb - 1 was in, and multiplies.  Blocks
+// past the last load that one again, so that the count is the same throughout.
+// Same MFMAs, folds and order as the other kernels: the sums are theirs bit for bit.
+constexpr int MID_BM = 64, MID_BN = 128, MID_STAGES = 3, MID_DMA = 4;   // MID_DMA: a wave's DMA per block
+constexpr int MID_STAGE = (MID_BM + MID_BN) * BK + 8 * 256;
+__shared__ __attribute__((aligned(1024))) uint8_t sM0[MID_STAGE];
+__shared__ __attribute__((aligned(1024))) uint8_t sM1[MID_STAGE];
+__shared__ __attribute__((aligned(1024))) uint8_t sM2[MID_STAGE];
+template <int ST> __device__ __forceinline__ uint8_t *stM() {
+    return ST == 0 ? sM0 : ST == 1 ? sM1 : sM2;
+}
+
+struct MidLoader {
+    __amdgpu_buffer_rsrc_t rA, rB, rS;
+    int offA, offB[2], offS, wave;
+};
+
+// The row in LDS slot s (lds_slot inverted).
+__device__ __forceinline__ int slot_row(int s) { return (s & ~15) | ((s & 15) >> 1) | ((s & 1) << 3); }
+
+template <int ST>
+__device__ __forceinline__ void mid_load(const MidLoader &L, int kb) {
+    uint8_t *st = stM<ST>();
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(L.rA, (lds_void *)(st + L.wave * 1024), 16, L.offA, kb * BK, 0, 0);
 #pragma unroll
-        for (int i = 0; i < RG; i++) {
-            idr[i] = __shfl(id, 16 * i + frow, 64);
-            s[i] = q.lora.scale ? q.lora.scale[max(idr[i], 0)] : 1.0f;
-        }
-        for (int r0 = 0; r0 < R; r0 += 32) {
-            const int r = r0 + 8 * fg;
-            v8bf hi[RG], lo[RG];
+    for (int i = 0; i < 2; i++)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(L.rB, (lds_void *)(st + MID_BM * BK + (2 * L.wave + i) * 1024), 16,
+                                                 L.offB[i], kb * BK, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(L.rS, (lds_void *)(st + (MID_BM + MID_BN) * BK + L.wave * 256), 4, L.offS,
+                                             kb * 4, 0, 0);
+}
+
+template <int ST>
+__device__ __forceinline__ void mid_block(v4f (&acc)[2][2], const MidLoader &L, int kb, int KB, const float *sb, int lane) {
+    const int frow = lane & 15, fg = lane >> 4, wm = L.wave >> 2, wn = L.wave & 3;
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (MID_DMA * (MID_STAGES - 2)));   // vmcnt: block kb is in
+    barrier_lds_only();
+    mid_load<(ST + MID_STAGES - 1) % MID_STAGES>(L, min(kb + MID_STAGES - 1, KB - 1));
+    const uint8_t *st = stM<ST>();
+    const float *sc = (const float *)(st + (MID_BM + MID_BN) * BK + L.wave * 256);
+    const float sbk = sb[kb];
+    v8i a[2], b[2];
+    float s[2];
 #pragma unroll
-            for (int i = 0; i < RG; i++)
-                lora_split(lora_load_h(q.lora, m0 + 16 * i + frow, idr[i] >= 0, r), s[i], hi[i], lo[i]);
-            uint64_t todo = all;
-            while (todo) {
-                int a[4];
-                v8bf b[4][CG];
-#pragma unroll
-                for (int t = 0; t < 4; t++) {
-                    a[t] = -2;   // no row's
-                    if (!todo) continue;
-                    a[t] = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)todo) - 1);
-                    todo &= ~__ballot(id == a[t]);
-                    const __amdgpu_buffer_rsrc_t rL = lora_rsrc(q.lora, a[t], n, g.N);
-#pragma unroll
-                    for (int j = 0; j < CG; j++) b[t][j] = lora_load_b(rL, lora_col(j, frow), r, R);
-                }
-#pragma unroll
-                for (int t = 0; t < 4; t++) {
-                    if (a[t] < 0) continue;
-#pragma unroll
-                    for (int i = 0; i < RG; i++) {
-                        const u32x4 z = {0u, 0u, 0u, 0u};
-                        const v8bf h = __builtin_bit_cast(v8bf, idr[i] == a[t] ? __builtin_bit_cast(u32x4, hi[i]) : z);
-                        const v8bf l = __builtin_bit_cast(v8bf, idr[i] == a[t] ? __builtin_bit_cast(u32x4, lo[i]) : z);
-#pragma unroll
-                        for (int j = 0; j < CG; j++) {
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], h, acc[i][j], 0, 0, 0);
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], l, acc[i][j], 0, 0, 0);
-                        }
-                    }
-                }
-            }
-        }
+    for (int i = 0; i < 2; i++) {
+        a[i] = lds_frag(st, wm * 32 + i * 16 + frow, fg);
+        b[i] = lds_frag(st + MID_BM * BK, wn * 32 + i * 16 + frow, fg);
+        s[i] = sc[wm * 32 + i * 16 + frow] * sbk;
     }
+    v4f p[2][2];
 #pragma unroll
-    for (int i = 0; i < RG; i++) {
-        if (16 * i + frow >= rows_in) continue;
-        const uint32_t m = (uint32_t)(m0 + 16 * i + frow), br = (uint32_t)g.band_rows, d = m / br;
-        uint16_t *row = g.C + (int64_t)d * g.band_stride + (int64_t)(m - d * br) * g.N + n + 8 * fg;
+    for (int i = 0; i < 2; i++)
 #pragma unroll
-        for (int j = 0; j < CG; j += 2) {
-            const u32x4 o = {pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]),
-                             pack_bf16x2(acc[i][j + 1][0], acc[i][j + 1][1]),
-                             pack_bf16x2(acc[i][j + 1][2], acc[i][j + 1][3])};
-            *(u32x4 *)(row + 16 * j) = o;
-        }
+        for (int j = 0; j < 2; j++)
+            p[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[i], (v4f){0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0,
+                                                                       0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) fold4(acc[i][j], p[i][j], s[i]);
+}
+
+__global__ void __launch_bounds__(NTHREADS) bsgemm_lora_mid_kernel(GemmArgs g, LoraGemmArgs q) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // the row tiles of one column block follow each other on one XCD
+    const int tm = (int)((g.M + MID_BM - 1) / MID_BM);
+    const int turn = blockIdx.x / NUM_XCD;
+    const int64_t m0 = (int64_t)(turn % tm) * MID_BM;
+    const int64_t n0 = ((int64_t)(turn / tm) * NUM_XCD + blockIdx.x % NUM_XCD) * MID_BN;
+    if (n0 >= g.N) return;
+    const int rows_in = (int)(g.M - m0 < MID_BM ? g.M - m0 : MID_BM);
+    const int K = (int)g.K, KB = g.KB;
+    MidLoader L;
+    L.wave = wave;
+    L.rA = make_rsrc(g.A + m0 * K, (int64_t)rows_in * K);
+    L.rB = make_rsrc(g.B + n0 * K, (int64_t)MID_BN * K);
+    L.rS = make_rsrc((const float *)g.sa + m0 * KB, (int64_t)rows_in * KB * 4);
+    const int ra = slot_row(8 * wave + (lane >> 3));
+    L.offA = ra * K + ((lane & 7) ^ (ra & 7)) * 16;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        // LDS row r holds B row lora_col of its sub-tile, within the wave's 32 columns
+        const int r = slot_row(8 * (2 * wave + i) + (lane >> 3));
+        L.offB[i] = ((r & ~31) + lora_col((r >> 4) & 1, r & 15)) * K + ((lane & 7) ^ (r & 7)) * 16;
     }
+    L.offS = lane * KB * 4;
+    const float *sb = (const float *)g.sb + n0 / 128 * KB;
+    v4f acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+    mid_load<0>(L, 0);
+    mid_load<1>(L, min(1, KB - 1));
+    for (int kb = 0; kb < KB; kb += MID_STAGES) {
+        mid_block<0>(acc, L, kb, KB, sb, lane);
+        if (kb + 1 < KB) mid_block<1>(acc, L, kb + 1, KB, sb, lane);
+        if (kb + 2 < KB) mid_block<2>(acc, L, kb + 2, KB, sb, lane);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the DMA past the last block is retired
+    const int64_t mw = m0 + 32 * (wave >> 2), nw = n0 + 32 * (wave & 3);
+    const int rw = rows_in - 32 * (wave >> 2);
+    if (rw <= 0) return;
+    wave_adapters<2, 2>(acc, g, q, mw, nw, rw < 32 ? rw : 32, lane);
+    wave_store<2, 2>(acc, g, mw, nw, rw < 32 ? rw : 32, lane);
 }
 
 // B [N, K] -> the prepacked layout [N/16][K/128][2][64][16 B]: unit u of the
@@ -1746,20 +1881,23 @@ int bs_launch_gemm_lora(const uint8_t *A, const float *sa, const uint8_t *B, con
                         int64_t band_stride, hipStream_t stream) {
     const GemmArgs g = gemm_args(A, sa, B, sb, C, M, N, K, band_rows, band_stride);
     const LoraGemmArgs q = {lora, ids};
-    // Short batches by waves of 16 x 32, 32 x 64 or 64 x 64, whichever is the first to
-    // need at most 512 of them (two to a CU): a smaller wave tile waits less, a
-    // larger one reads less.  K = 2048, R = 16, us by graph launches, for the three
-    // and the 256-row tile: N = 7168, M = 16: 9.0 / 12.8 / 19.2 / 27.0; M = 64: 19.3 /
-    // 13.9 / 21.2 / 28.5; M = 256: 58 / 34 / 26 / 34; M = 384: 96 / 49 / 36 / 34;
-    // N = 1024, M = 256: 11.1 / 12.4 / 19.4 / 31.0; M = 1024: 35 / 19.5 / 22 / 33.
-    const auto waves = [&](int rows, int cols) { return N / cols * ((M + rows - 1) / rows); };
-    const auto run_short = [&](auto kernel, int rows, int cols) {
-        const int64_t blocks = (N / cols + NUM_XCD - 1) / NUM_XCD * NUM_XCD * ((M + rows - 1) / rows);
-        return bs_enqueue(kernel, dim3((unsigned)blocks), dim3(64), stream, g, q);
+    // Short batches by waves of 16 x 32 or 32 x 64 while that takes at most two or one
+    // of them to a CU, middling ones by 64 x 128 tiles while that takes at most two.
+    // K = 2048, R = 16, us by graph launches, 16 x 32 / 32 x 64 / 64 x 128 / 256 x 256:
+    // N = 7168, M = 16: 9.0 / 12.8 / 13.4 / 27.0; M = 64: 19.3 / 13.9 / 15.5 / 28.5;
+    // M = 200: 50 / 34 / 15.5 / 32; M = 512: 112 / 57 / 22 / 34; M = 1024: 220 / 122 /
+    // 41 / 35; N = 1024, M = 256: 11.1 / 12.4 / 11.8 / 31; M = 512: 19.4 / 13.8 / 15.4 /
+    // 31; M = 2048: - / - / 16.9 / 27; M = 4096: - / - / 25 / 34.
+    const auto grid_of = [&](int rows, int cols) {
+        return dim3((unsigned)((N / cols + NUM_XCD - 1) / NUM_XCD * NUM_XCD * ((M + rows - 1) / rows)));
     };
-    if (waves(16, 32) <= 512) return run_short(bsgemm_lora_short_kernel<1, 2, 4>, 16, 32);
-    if (waves(32, 64) <= 512) return run_short(bsgemm_lora_short_kernel<2, 4, 3>, 32, 64);
-    if (waves(64, 64) <= 512) return run_short(bsgemm_lora_short_kernel<4, 4, 2>, 64, 64);
+    const auto count = [&](int rows, int cols) { return N / cols * ((M + rows - 1) / rows); };
+    if (count(16, 32) <= 512)
+        return bs_enqueue(bsgemm_lora_short_kernel<1, 2, 4>, grid_of(16, 32), dim3(64), stream, g, q);
+    if (count(32, 64) <= 256)
+        return bs_enqueue(bsgemm_lora_short_kernel<2, 4, 3>, grid_of(32, 64), dim3(64), stream, g, q);
+    if (count(MID_BM, MID_BN) <= 512)
+        return bs_enqueue(bsgemm_lora_mid_kernel, grid_of(MID_BM, MID_BN), dim3(NTHREADS), stream, g, q);
     return bs_enqueue(bsgemm_lora_tile_kernel, dim3(gemm_grid(g)), dim3(NTHREADS), stream, g, q);
 }
 

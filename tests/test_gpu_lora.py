@@ -258,7 +258,8 @@ GEMM = [(1, 128, 128, 1, 8, 1, 0), (1, 7168, 2048, 16, 16, 1, 0), (15, 384, 640,
         (17, 256, 896, 2, 64, 1, 0), (33, 1152, 512, 40, 24, 3, 0), (64, 640, 384, 64, 72, 8, 0),
         (65, 512, 256, 3, 128, 13, 5 * 512 + 16), (256, 768, 1024, 5, 16, 2, 0), (257, 768, 1024, 5, 16, 1, 0), (16, 128, 256, 3, 16, 1, 0), (200, 384, 256, 4, 16, 4, 50 * 384 + 64),
         (300, 640, 384, 70, 64, 3, 0), (513, 512, 1152, 5, 128, 1, 0), (1040, 1280, 512, 2, 40, 8, 0),
-        (520, 1024, 384, 3, 48, 4, 0), (2050, 2304, 128, 3, 16, 1, 0), (2100, 2304, 384, 4, 72, 7, 0),
+        (520, 1024, 384, 3, 48, 4, 0), (264, 1024, 128, 3, 16, 1, 0), (1000, 1024, 256, 9, 72, 5, 0),
+        (700, 2176, 640, 70, 32, 7, 100 * 2176 + 8), (1537, 1280, 896, 4, 8, 1, 0), (2050, 2304, 128, 3, 16, 1, 0), (2100, 2304, 384, 4, 72, 7, 0),
         (2600, 5120, 256, 6, 24, 8, 0), (2056, 2304, 512, 9, 256, 8, 257 * 2304 + 8)]
 
 
