@@ -871,16 +871,16 @@ struct LoraGemmArgs {
 // A wave goes through the distinct adapters of its 128 rows (one or two in a
 // prefill chunk, whose requests are runs of rows).  For each it has the
 // adapter's 64 columns of B in registers, in the sub-tiles' own column order,
-// and gives every 16-row group that has such a row its products, with zeros in
-// the rows of other adapters.  A group without one is skipped, so a row of no
-// adapter keeps its product bit for bit unless it shares a group with others',
-// where it gets a zero added, which changes nothing but the sign of a zero.
+// and gives every 16-row group that has such a row its products, which only the
+// adapter's own rows keep: a row takes nothing from another adapter, be its weights
+// NaN, and a row of no adapter keeps its product bit for bit.
 //
 // Measured at M = 16384, N = 7168, K = 2048, 8 adapters in runs, against 213 us
-// without adapters: R = 16 / 64 / 128: 239 / 250 / 285 us; every row its own
-// draw of the 8 adapters, R = 64: 371.  What is left at R = 64 is B's latency
-// (14 us), the split (7), the second product (5) and the fragments' reads (5),
-// from copies with one of them left out.  This stands in the tile kernel:
+// without adapters: R = 16 / 64 / 128: 235 / 253 / 287 us; every row its own
+// draw of the 8 adapters, R = 64: 401 (keeping other rows' sums took 3 and 34 us
+// over adding them zeros, which let one adapter's NaN into its neighbours).  What
+// is left at R = 64 is B's latency (14 us), the split (7), the second product (5)
+// and the fragments' reads (5), from copies with one of them left out.  This stands in the tile kernel:
 // in the persistent one it spilled 64 to 95 registers and took 277 us.
 
 // ids of the tile's rows, loaded with the tile's first K block
@@ -1004,18 +1004,17 @@ __device__ __forceinline__ void lora_chunk(v4f (&acc)[TM][TN], LoraWave &w, cons
             const bool live = (rows >> frow) & 1;
             const uint8_t *st = h ? stB<ST>() : stA<ST>();
             const int r = wm * WM + 16 * i + frow;
-            u32x4 hi = *(const u32x4 *)(st + swz(r, 2 * fg)), lo = *(const u32x4 *)(st + swz(r, 2 * fg + 1));
+            const v8bf hi = *(const v8bf *)(st + swz(r, 2 * fg)), lo = *(const v8bf *)(st + swz(r, 2 * fg + 1));
+            v4f t[TN];
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                hi[e] = live ? hi[e] : 0u;
-                lo[e] = live ? lo[e] : 0u;
-            }
+            for (int j = 0; j < TN; j++) t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], hi, acc[i][j], 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < TN; j++)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, hi), acc[i][j], 0, 0, 0);
+            for (int j = 0; j < TN; j++) t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], lo, t[j], 0, 0, 0);
+            // a lane's sums are those of row frow: other adapters' rows keep theirs
 #pragma unroll
             for (int j = 0; j < TN; j++)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], __builtin_bit_cast(v8bf, lo), acc[i][j], 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[i][j][e] = live ? t[j][e] : acc[i][j][e];
         }
     };
     if (w.first < 0) return;
@@ -1573,13 +1572,14 @@ __device__ __forceinline__ void wave_adapters(v4f (&acc)[RG][CG], const GemmArgs
                     if (a[t] < 0) continue;
 #pragma unroll
                     for (int i = 0; i < RG; i++) {
-                        const u32x4 z = {0u, 0u, 0u, 0u};
-                        const v8bf h = __builtin_bit_cast(v8bf, idr[i] == a[t] ? __builtin_bit_cast(u32x4, hi[i]) : z);
-                        const v8bf l = __builtin_bit_cast(v8bf, idr[i] == a[t] ? __builtin_bit_cast(u32x4, lo[i]) : z);
+                        // a lane's sums are those of row frow: other adapters' rows keep theirs
+                        const bool live = idr[i] == a[t];
 #pragma unroll
                         for (int j = 0; j < CG; j++) {
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], h, acc[i][j], 0, 0, 0);
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], l, acc[i][j], 0, 0, 0);
+                            v4f x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], hi[i], acc[i][j], 0, 0, 0);
+                            x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][j], lo[i], x, 0, 0, 0);
+#pragma unroll
+                            for (int e = 0; e < 4; e++) acc[i][j][e] = live ? x[e] : acc[i][j][e];
                         }
                     }
                 }

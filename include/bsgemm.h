@@ -338,6 +338,10 @@ bs_status band_rowq_e4m3(const uint16_t *const *parts, int32_t P, uint8_t *q,
  *
  * One plan serves every layer that the batch passes through.
  *
+ * Rows are apart in all of these calls: a value that is not finite, in a row or
+ * in the adapter that it uses, makes that row's results non-finite, and no
+ * other row's.
+ *
  *   ids   int32 [M] (may be null when M = 0)
  *   plan  int32 [n_adapters + 2 + M]
  *
@@ -354,9 +358,8 @@ bs_status lora_plan(const int32_t *ids, int32_t *plan, int64_t M, int64_t n_adap
  * bsgemm_fp8_lora add it to the same GPU's partial output, whose reduction then
  * completes both.
  *
- *   x     bf16 [M, K] (finite)
- *   A     bf16 [n_adapters, R, K] (finite; an adapter of a smaller rank has
- *         zero rows)
+ *   x     bf16 [M, K]
+ *   A     bf16 [n_adapters, R, K] (an adapter of a smaller rank has zero rows)
  *   plan  as lora_plan writes it for these rows and n_adapters.  Entries that
  *         lie outside the batch are ignored, but no check finds that a plan
  *         belongs to another batch
@@ -379,8 +382,8 @@ bs_status lora_shrink(const uint16_t *x, const uint16_t *A, const int32_t *plan,
  * out are row-banded as bsgemm_fp8's C (bands, band_stride as there); elements
  * between bands are untouched.  out may be base itself.
  *
- *   H      fp32 [M, R] (finite; the rows without an adapter are not read)
- *   B      bf16 [n_adapters, N, R] (finite)
+ *   H      fp32 [M, R] (what rows without an adapter hold does not matter)
+ *   B      bf16 [n_adapters, N, R]
  *   scale  fp32 [n_adapters] or null (1)
  *   plan   as for lora_shrink
  *   base   bf16 bands;  out  bf16 bands
@@ -398,14 +401,14 @@ bs_status lora_expand(const float *H, const uint16_t *B, const float *scale, con
  * bsgemm_fp8 with its rows' adapters: to the finished fp32 accumulator of row m
  * is added scale[a] * sum_r H[m, r] * lora_B[a, n, r], a = ids[m], before the one
  * rounding to bf16.  A row whose id is outside [0, n_adapters) gets bsgemm_fp8's
- * result, bit for bit (the sign of a zero apart), and its H is not read.  This
- * reads ids directly and needs no plan: prefer it to bsgemm_fp8 followed by
- * lora_expand, which writes and reads C once more; its cost grows with the
- * number of different adapters among 128 consecutive rows.
+ * result, bit for bit, whatever its H holds.  This reads ids directly and needs no
+ * plan: prefer it to bsgemm_fp8 followed by lora_expand, which writes and reads C
+ * once more.  Its cost grows with the number of different adapters among 128
+ * consecutive rows: keep a long batch in runs of rows that share one.
  *
  *   A, a_scale, B, b_scale, C, bands, band_stride  as for bsgemm_fp8
- *   H           fp32 [M, R] (finite), from lora_shrink
- *   lora_B      bf16 [n_adapters, N, R] (finite)
+ *   H           fp32 [M, R], from lora_shrink
+ *   lora_B      bf16 [n_adapters, N, R]
  *   lora_scale  fp32 [n_adapters] or null (1)
  *   ids         int32 [M]
  *

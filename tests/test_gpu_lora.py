@@ -281,7 +281,7 @@ def test_gemm_exact_integers(M, N, K, L, R, bands, stride):
         d, _ = opsref.delta(H.astype(float), B.astype(float), scale, ids)
         assert np.array_equal(values(got), bounds.bf16_rne_f64(acc + d)), mix
         none = to_dev((ids < 0) | (ids >= L))
-        assert torch.equal(got[none].float(), plain[none].float())
+        assert torch.equal(got[none].view(torch.int16), plain[none].view(torch.int16))
 
 
 @pytest.mark.parametrize("M,N,K,L,R", [(5, 384, 1152, 4, 48), (200, 512, 256, 4, 16), (700, 1024, 640, 3, 64), (1300, 1280, 512, 8, 32),
@@ -347,3 +347,44 @@ def test_gemm_full_size_against_its_parts():
         # and opsref.delta's bound with the 2R additions onto the accumulator
         tol = 2.0 ** -8 * (p.abs() + c.abs()) + (2.0 ** -17 + 4 * opsref.U * R) * (S + p.abs()) + 1e-30
         assert bool(((c - p - d).abs() <= tol).all()), a
+
+
+# ------------------------------------------------------------ rows apart --
+
+@pytest.mark.parametrize("M,N,K", [(50, 256, 256), (700, 512, 256), (1100, 1152, 256), (2300, 2304, 384)])
+def test_what_is_not_finite_stays_in_its_rows(M, N, K):
+    """One adapter's weights are NaN and infinite, one row's input is NaN, and rows of no
+    adapter hold NaN in H: those rows come out non-finite, every other one as it does without."""
+    say(f"not finite: M={M} N={N} K={K}")
+    L, R = 5, 40
+    rng = np.random.default_rng(M)
+    ids = rng.integers(-1, L, M).astype(np.int32)
+    x, A = bf(rng.standard_normal((M, K))), bf(rng.standard_normal((L, R, K)))
+    B = bf(rng.standard_normal((L, N, R)))
+    ops = tuple(to_dev(a) for a in gemm_operands(M, N, K, 1, False))
+    base = bf(rng.standard_normal((M, N))).view(-1)
+    di = to_dev(ids)
+    plan = bs.lora_plan(di, L)
+
+    def run(x, A, B, H=None):
+        h = bs.lora_shrink(x, A, plan) if H is None else H
+        return h, bs.lora_expand(h, B, plan, base).view(M, N), bs.bsgemm_fp8_lora(*ops, h, B, di).view(M, N)
+    want = run(x, A, B)
+    bad_row = int(np.flatnonzero(ids == 1)[0])
+    x2, A2, B2 = x.clone(), A.clone(), B.clone()
+    x2[bad_row, 3] = float("nan")
+    A2[3, 2, 5] = float("inf")
+    B2[4, :, 0] = float("nan")
+    got = run(x2, A2, B2)
+    H3 = want[0].clone()
+    H3[di < 0] = float("nan")
+    again = run(x, A, B, H3)
+    torch.cuda.synchronize()
+    hit = (ids == 3) | (np.arange(M) == bad_row)
+    for k, (g, w) in enumerate(zip(got, want)):
+        bad = hit | ((ids == 4) if k else False)
+        ok = to_dev(~bad)
+        assert torch.equal(g[ok].view(torch.uint8), w[ok].view(torch.uint8)), k
+        assert not bool(torch.isfinite(g[to_dev(bad)]).all(1).any()), k
+    for g, w in list(zip(again, want))[1:]:
+        assert torch.equal(g.view(torch.uint8), w.view(torch.uint8))

@@ -57,9 +57,8 @@ def test_expand_and_gemm():
     bs.bsgemm_fp8_lora(qa, sa, qb, sb, H, B, ids, C=out)
     want = bs.bsgemm_fp8_lora(qa[rows], sa[rows], qb, sb, H[rows], B, few)
     torch.cuda.synchronize()
-    # the small batch's kernel groups rows differently; sums are the same, and a
-    # zero added to a row of no adapter may change the sign of a zero
-    assert torch.equal(out.view(M, N)[rows].float(), want.view(-1, N).float())
+    # another kernel, which adds in the same order
+    assert same(out.view(M, N)[rows], want.view(-1, N))
 
 
 def test_shrink():

@@ -199,3 +199,31 @@ def test_empty_batches():
                               e(0, 16, dtype=f32), e(3, 128, 16), e(0, dtype=i32)).numel() == 0
     r, z, q, sc = bs.resnorm(e(0, 256), e(0, 256), quant=128)
     assert r.shape == (0, 256) and z is None and q.shape == (0, 256) and sc.shape == (0, 2)
+
+
+def test_refusals_on_the_device():
+    """What only device tensors can show: strides, types, and tensors that are not there."""
+    say("refusals of device tensors")
+    d = device()
+    x = torch.zeros((8, 128), dtype=torch.bfloat16, device=d)
+    A = torch.zeros((2, 16, 128), dtype=torch.bfloat16, device=d)
+    plan = bs.lora_plan(torch.zeros(8, dtype=torch.int32, device=d), 2)
+    wide = torch.zeros((8, 256), dtype=torch.bfloat16, device=d)
+    with pytest.raises(ValueError, match="contiguous"):
+        bs.lora_shrink(wide[:, ::2], A, plan)
+    with pytest.raises(ValueError, match="contiguous"):
+        bs.resnorm(wide[:, :128], x)
+    with pytest.raises(TypeError, match="dtype"):
+        bs.lora_shrink(x.half(), A, plan)
+    with pytest.raises(TypeError, match="dtype"):
+        bs.lora_plan(torch.zeros(8, dtype=torch.int64, device=d), 2)
+    with pytest.raises(TypeError, match="dtype"):
+        bs.resnorm(x, x.half())
+    with pytest.raises(ValueError, match="device tensor"):
+        bs.lora_shrink(x, A.cpu(), plan)
+    with pytest.raises(bs.BSError):   # 16-byte alignment
+        bs.resnorm(wide.view(-1)[4:4 + 1024].view(8, 128), x)
+    with pytest.raises(bs.BSError):   # the output over an input
+        bs.lora_shrink(x, A, plan, x.view(torch.float32).view(-1)[:128].view(8, 16))
+    with pytest.raises(bs.BSError):
+        bs.resnorm(x, x, eps=0.0)
