@@ -1514,6 +1514,23 @@ __global__ void __launch_bounds__(NTHREADS) mxgemm_tile_kernel(GemmArgs g) { gem
 // side by side took 1.3 to 2.5 times as long: they wait on one CU).  Each K block is the same MFMA on the same fragments, folded in the same order, so the
 // sums are those of the other kernels bit for bit.  The 16-column sub-tiles take B's
 // rows in the order of lora_col, two sub-tiles to a 16-byte piece of C.
+// Workgroup -> tile of rows x cols.  Workgroups are dealt to the XCDs in turn, and a
+// column's row tiles follow each other on one XCD, whose L2 serves B to all but the
+// first.  Where the columns divide by the XCDs they are dealt in turn, which reads
+// the weight evenly (N = 7168: M = 1 7.1 us, M = 64 14.2, against 7.7 and 15.1 by
+// runs); otherwise each XCD gets a contiguous run of tiles, so that none idles
+// (N = 384, K = 256, M = 5733: 9.6 us against 16.0).  False for the workgroups past
+// the last tile.
+__device__ __forceinline__ bool column_tile(const GemmArgs &g, int rows, int cols, int64_t &m0, int64_t &n0) {
+    const int tm = (int)((g.M + rows - 1) / rows), tn = (int)(g.N / cols);
+    const int xcd = (int)(blockIdx.x % NUM_XCD), turn = (int)(blockIdx.x / NUM_XCD);
+    const bool even = tn % NUM_XCD == 0;
+    const int t = even ? turn : xcd * (int)(gridDim.x / NUM_XCD) + turn;
+    m0 = (int64_t)(t % tm) * rows;
+    n0 = (int64_t)(even ? t / tm * NUM_XCD + xcd : t / tm) * cols;
+    return n0 < g.N;
+}
+
 template <int RG, int CG>
 struct ShortBlock {
     v8i a[RG], b[CG];
@@ -1611,14 +1628,8 @@ template <int RG, int CG, int D>
 __global__ void __launch_bounds__(64) bsgemm_lora_short_kernel(GemmArgs g, LoraGemmArgs q) {
     const int lane = threadIdx.x;
     const int frow = lane & 15, fg = lane >> 4;
-    // workgroups are dealt to the XCDs in turn: the row tiles of one column block
-    // follow each other on one XCD, whose L2 then serves B to all but the first
-    const int tm = (int)((g.M + 16 * RG - 1) / (16 * RG));
-    const int turn = blockIdx.x / NUM_XCD;
-    const int cb = turn / tm * NUM_XCD + (int)(blockIdx.x % NUM_XCD);
-    const int64_t m0 = (int64_t)(turn % tm) * (16 * RG);
-    const int64_t n = (int64_t)cb * (16 * CG);
-    if (n >= g.N) return;
+    int64_t m0, n;
+    if (!column_tile(g, 16 * RG, 16 * CG, m0, n)) return;
     const int rows_in = (int)(g.M - m0 < 16 * RG ? g.M - m0 : 16 * RG);
     const int K = (int)g.K, KB = g.KB;
     const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.A + m0 * K, (int64_t)rows_in * K);
@@ -1752,12 +1763,8 @@ __device__ __forceinline__ void mid_block(v4f (&acc)[2][2], const MidLoader &L, 
 __global__ void __launch_bounds__(NTHREADS) bsgemm_lora_mid_kernel(GemmArgs g, LoraGemmArgs q) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // the row tiles of one column block follow each other on one XCD
-    const int tm = (int)((g.M + MID_BM - 1) / MID_BM);
-    const int turn = blockIdx.x / NUM_XCD;
-    const int64_t m0 = (int64_t)(turn % tm) * MID_BM;
-    const int64_t n0 = ((int64_t)(turn / tm) * NUM_XCD + blockIdx.x % NUM_XCD) * MID_BN;
-    if (n0 >= g.N) return;
+    int64_t m0, n0;
+    if (!column_tile(g, MID_BM, MID_BN, m0, n0)) return;
     const int rows_in = (int)(g.M - m0 < MID_BM ? g.M - m0 : MID_BM);
     const int K = (int)g.K, KB = g.KB;
     MidLoader L;
@@ -1888,10 +1895,10 @@ int bs_launch_gemm_lora(const uint8_t *A, const float *sa, const uint8_t *B, con
     // M = 200: 50 / 34 / 15.5 / 32; M = 512: 112 / 57 / 22 / 34; M = 1024: 220 / 122 /
     // 41 / 35; N = 1024, M = 256: 11.1 / 12.4 / 11.8 / 31; M = 512: 19.4 / 13.8 / 15.4 /
     // 31; M = 2048: - / - / 16.9 / 27; M = 4096: - / - / 25 / 34.
-    const auto grid_of = [&](int rows, int cols) {
-        return dim3((unsigned)((N / cols + NUM_XCD - 1) / NUM_XCD * NUM_XCD * ((M + rows - 1) / rows)));
-    };
     const auto count = [&](int rows, int cols) { return N / cols * ((M + rows - 1) / rows); };
+    const auto grid_of = [&](int rows, int cols) {
+        return dim3((unsigned)((count(rows, cols) + NUM_XCD - 1) / NUM_XCD * NUM_XCD));
+    };
     if (count(16, 32) <= 512)
         return bs_enqueue(bsgemm_lora_short_kernel<1, 2, 4>, grid_of(16, 32), dim3(64), stream, g, q);
     if (count(32, 64) <= 256)
