@@ -516,7 +516,12 @@ def bsgemm_fp8_lora(A, a_scale, B, b_scale, H, lora_B, ids, scale=None, C=None, 
     """bsgemm_fp8 plus scale[a] * (H [M,R] fp32 x lora_B[a]^T) for each row's adapter a = ids[row]
     (lora_B bf16 [n_adapters,N,R]), added in fp32 before the rounding to bf16."""
     ty = _ty()
-    M, N, K = _check_gemm_operands(A, a_scale, B, b_scale, 128, "bsgemm_fp8_lora")
+    M, K = _matrix(A, "A")
+    N = _matrix(B, "B")[0]
+    if B.shape[1] != K or K % 128 or N % 128:
+        raise ValueError(f"bsgemm_fp8_lora: A is [M,{K}], B {tuple(B.shape)}: one K, and K and N multiples of 128")
+    _is(a_scale, (M, K // 128), "a_scale")
+    _is(b_scale, (N // 128, K // 128), "b_scale")
     Mh, _, L, R = _check_lora(H, lora_B, scale, N, "lora_B")
     if not (Mh == M):
         raise ValueError(f"H: {Mh} rows, A has {M}")

@@ -457,6 +457,11 @@ static int launch_expand_r(const ExpandArgs &g, hipStream_t stream) {
 int bs_launch_lora_expand(const LoraArgs &lora, const int32_t *plan, const uint16_t *base, uint16_t *out, int64_t M,
                           int64_t N, int64_t band_rows, int64_t band_stride, hipStream_t stream) {
     const ExpandArgs g = {lora, plan, base, out, (int)M, (int)band_rows, 0, 0, N, band_stride - band_rows * N};
-    if (M >= 64 * (int64_t)(lora.L + 1)) return launch_expand_r<4>(g, stream);
+    // 64-row tiles once an adapter has 32 rows on average and there is work for every
+    // CU.  R = 64, rows mixed, 16-row tiles / 64-row, us by graph launches: N = 7168, 8
+    // adapters, M = 128: 8.4 / 8.7, 512: 13.0 / 10.5, 2048: 31.5 / 23.5; 32 adapters,
+    // M = 512: 17.6 / 19.1, 2048: 42.7 / 27.1; N = 1024, M = 512: 5.3 / 7.9, 2048: 8.0 /
+    // 8.4, 8192: 19.6 / 14.1.  32-row tiles lie between the two.
+    if (M >= 32 * (int64_t)(lora.L + 1) && M * N >= (int64_t)1 << 21) return launch_expand_r<4>(g, stream);
     return launch_expand_r<1>(g, stream);
 }

@@ -183,7 +183,8 @@ def run_expand(H, B, ids, base, scale=None, bands=1, stride=0, inplace=False):
 
 EXPAND = [(1, 8, 1, 8, 1, 0), (1, 7168, 3, 16, 1, 0), (37, 1000, 32, 16, 1, 0), (48, 264, 5, 40, 4, 12 * 264 + 64),
           (64, 512, 70, 64, 8, 0), (300, 136, 4, 128, 3, 100 * 136 + 8), (90, 512, 2, 256, 1, 0),
-          (2100, 520, 3, 64, 7, 0), (4500, 72, 5, 24, 1, 0)]
+          (2100, 520, 3, 64, 7, 0), (4500, 72, 5, 24, 1, 0), (1000, 2312, 4, 24, 8, 125 * 2312 + 8),
+          (300, 7168, 3, 128, 1, 0), (290, 7688, 2, 256, 2, 145 * 7688 + 8), (2400, 7176, 3, 40, 1, 0)]
 
 
 @pytest.mark.parametrize("M,N,L,R,bands,stride", EXPAND)

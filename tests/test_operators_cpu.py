@@ -145,6 +145,10 @@ def test_binding_refusals():
     refused("device tensor", bs.lora_expand, H, B, pl, base)
     g = (t(64, 256, dtype=u8), t(64, 2, dtype=f32), t(512, 256, dtype=u8), t(4, 2, dtype=f32))
     refused("a_scale", bs.bsgemm_fp8_lora, g[0], t(64, 3, dtype=f32), *g[2:], H, B, ids)
+    refused("b_scale", bs.bsgemm_fp8_lora, *g[:3], t(2, 4, dtype=f32), H, B, ids)
+    refused("one K", bs.bsgemm_fp8_lora, *g[:2], t(512, 128, dtype=u8), g[3], H, B, ids)
+    refused("multiples", bs.bsgemm_fp8_lora, *g[:2], t(500, 256, dtype=u8), g[3], H, B, ids)
+    refused("A must", bs.bsgemm_fp8_lora, g[0].view(-1), *g[1:], H, B, ids)
     refused("H:", bs.bsgemm_fp8_lora, *g, t(32, 16, dtype=f32), B, ids)
     refused("lora_B:", bs.bsgemm_fp8_lora, *g, H, t(8, 256, 16), ids)
     refused("ids:", bs.bsgemm_fp8_lora, *g, H, B, t(63, dtype=i32))
