@@ -15,7 +15,7 @@
 // A row stays in its workgroup's registers from load to store, so each byte is
 // moved once: the kernel is bound by HBM.  16384 wire rows of 7168 with a bf16
 // residual to 1x128 codes: 121 us, 5.8 TB/s; 4096 bf16 rows of 5120 with an fp32
-// residual to bf16 and 1x32 codes: 57 us, 4.8 TB/s; one row of 7168: 4.4 us.
+// residual to bf16 and 1x32 codes: 50 us, 5.5 TB/s; one row of 7168: 4.4 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -107,8 +107,10 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
             yw[i] = __builtin_nontemporal_load((const u32x4 *)g.y + base + c);
         }
         if constexpr (RES32) {
-            ra[i] = __builtin_nontemporal_load((const u32x4 *)g.resid + 2 * (base + c));
-            rb[i] = __builtin_nontemporal_load((const u32x4 *)g.resid + 2 * (base + c) + 1);
+            // each of the two takes every other 16 bytes, so the lines have to stay in L1
+            // between them: non-temporal they took 56.6 us against 49.8 (4096 x 5120)
+            ra[i] = *((const u32x4 *)g.resid + 2 * (base + c));
+            rb[i] = *((const u32x4 *)g.resid + 2 * (base + c) + 1);
         } else {
             ra[i] = __builtin_nontemporal_load((const u32x4 *)g.resid + base + c);
         }
