@@ -53,20 +53,34 @@ __device__ __forceinline__ u32x4 narrow(const float (&v)[8]) {
     return o;
 }
 
-// The sum over a row's lanes: one wave (WAVE), or the workgroup's waves through
-// red.  A second use needs no barrier after the first one's reads: it takes
-// another slot.
-template <bool WAVE>
-__device__ __forceinline__ float row_sum(float v, float *red) {
+// The sum of a row's squares from each lane's P partial sums, one for every two of its
+// packs.  A row's 128 consecutive packs are summed over 64 lanes, two packs to each,
+// and those sums are added in the order of the packs: the same additions whether a
+// lane holds two packs (P = 1, a wave covers 128) or four (P = 2, 256), so a row's result
+// does not depend on how many rows the call has.  WAVE: the row is one wave's;
+// otherwise the workgroup's waves meet in red, another one for each use, which needs
+// no barrier after the reads.
+template <bool WAVE, int P>
+__device__ __forceinline__ float row_sum(float (&v)[P], float *red) {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-    if constexpr (!WAVE) {
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    for (int off = 32; off >= 1; off >>= 1)
+#pragma unroll
+        for (int h = 0; h < P; h++) v[h] += __shfl_xor(v[h], off, 64);
+    if constexpr (WAVE) {
+        static_assert(P == 1, "a wave's row has at most 128 packs");
+        return v[0];
+    } else {
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int h = 0; h < P; h++) red[(threadIdx.x >> 6) * P + h] = v[h];
+        }
         __syncthreads();
-        v = 0.f;
-        for (unsigned w = 0; w < blockDim.x / 64; w++) v += red[w];
+        float sum = 0.f;
+        for (unsigned w = 0; w < blockDim.x / 64; w++)
+#pragma unroll
+            for (int h = 0; h < P; h++) sum += red[w * P + h];
+        return sum;
     }
-    return v;
 }
 
 // amax over the G lanes of a scale block (G a power of two, blocks aligned)
@@ -77,9 +91,9 @@ __device__ __forceinline__ float group_max(float m) {
     return m;
 }
 
-// CPT packs of 8 values to a lane.  WAVE: a wave takes a row of up to 64 CPT
-// packs, four rows to a workgroup; otherwise the workgroup's T lanes take one of
-// up to T CPT (lane t the packs t + T i).  WIRE: y is e4m3 codes with a row scale.
+// CPT packs of 8 values to a lane, 64 CPT consecutive packs to a wave (lane l its
+// packs l + 64 i).  WAVE: a wave takes a whole row, four rows to a workgroup;
+// otherwise the workgroup's waves share one.  WIRE: y is e4m3 codes with a row scale.
 // RES32: the residual stream is fp32.  QB: 0, or the scale block of q.
 //
 // Every load, the weights' and the gate's too, goes out before the first
@@ -87,10 +101,11 @@ __device__ __forceinline__ float group_max(float m) {
 // stores nothing, so that no load is behind a branch.
 template <int CPT, bool WAVE, bool WIRE, bool RES32, int QB>
 __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
-    __shared__ float red[2][8];
-    const int T = WAVE ? 64 : (int)blockDim.x;
-    const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
-    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    constexpr int P = CPT / 2;   // partial sums of squares to a lane
+    __shared__ float red[2][8 * P];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int first = lane + (WAVE ? 0 : wave * 64 * CPT);
+    const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
     if (row >= g.rows) return;   // whole waves of a WAVE workgroup
     const int64_t base = row * g.nch;
     const float inv_n = 1.0f / (float)(g.nch * 8);
@@ -99,7 +114,7 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
     const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};   // bf16 1.0
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
-        const int c = min(tid + T * i, g.nch - 1);
+        const int c = min(first + 64 * i, g.nch - 1);
         if constexpr (WIRE) {
             const u32x2 q = __builtin_nontemporal_load((const u32x2 *)g.y + base + c);
             yw[i] = (u32x4){q[0], q[1], 0u, 0u};
@@ -118,7 +133,7 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
     const float ys = WIRE ? g.y_scale[row] : 1.0f;
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
-        const int c = min(tid + T * i, g.nch - 1);
+        const int c = min(first + 64 * i, g.nch - 1);
         pw[i] = g.post_w ? ((const u32x4 *)g.post_w)[c] : ones;
         gw[i] = g.gate ? *((const u32x4 *)(g.gate + row * g.gate_row) + c) : ones;
         ww[i] = g.pre_w ? ((const u32x4 *)g.pre_w)[c] : ones;
@@ -126,25 +141,28 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
 
     float v[CPT][8];
     float mul = g.beta;
-    float ss = 0.f;
+    float ss[P];
+#pragma unroll
+    for (int h = 0; h < P; h++) ss[h] = 0.f;
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
         if constexpr (WIRE) decode((u32x2){yw[i][0], yw[i][1]}, v[i]);
         else widen(yw[i], v[i]);
-        const float live = tid + T * i < g.nch ? 1.f : 0.f;
+        const float live = first + 64 * i < g.nch ? 1.f : 0.f;
         float sq = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; e++) {
             if (WIRE) v[i][e] *= ys;
             sq += v[i][e] * v[i][e];
         }
-        ss += live != 0.f ? sq : 0.f;
+        ss[i / 2] += live != 0.f ? sq : 0.f;
     }
     if (g.post_w) mul *= 1.0f / sqrtf(row_sum<WAVE>(ss, red[0]) * inv_n + g.eps);
-    ss = 0.f;
+#pragma unroll
+    for (int h = 0; h < P; h++) ss[h] = 0.f;
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
-        const int c = tid + T * i;
+        const int c = first + 64 * i;
         float p[8], q[8], r[8], sq = 0.f;
         widen(pw[i], p);
         widen(gw[i], q);
@@ -163,7 +181,7 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
             sq += v[i][e] * v[i][e];
         }
         if (c >= g.nch) continue;
-        ss += sq;
+        ss[i / 2] += sq;
         if constexpr (RES32) {
             u32x4 a, b;
 #pragma unroll
@@ -181,7 +199,7 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
     const float rs = 1.0f / sqrtf(row_sum<WAVE>(ss, red[1]) * inv_n + g.eps);
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
-        const int c = tid + T * i;
+        const int c = first + 64 * i;
         if (c >= g.nch) continue;   // whole scale blocks: N is a multiple of QB
         float w[8], amax = 0.f;
         widen(ww[i], w);

@@ -436,7 +436,7 @@ bs_status bsgemm_fp8_lora(const uint8_t *A, const float *a_scale, const uint8_t 
  *
  * All of it in fp32, each output rounded once: z and q come from the unrounded
  * h, and q from the unrounded z.  An all-zero scale block gets scale 0 (byte 0)
- * and codes 0x00.
+ * and codes 0x00.  A row's results do not depend on the other rows or their number.
  *
  *   y          bf16 [rows, N], or e4m3 [rows, N] with y_scale fp32 [rows]
  *   resid      bf16 [rows, N], or fp32 if resid_f32 is 1; resid_out the same
