@@ -83,11 +83,15 @@ __device__ __forceinline__ float row_sum(float (&v)[P], float *red) {
     }
 }
 
+// The larger of two values, NaN if either is (fmaxf drops NaN, and a block of
+// NaN would get the scale 0 of a block of zeros).
+__device__ __forceinline__ float nan_max(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // amax over the G lanes of a scale block (G a power of two, blocks aligned)
 template <int G>
 __device__ __forceinline__ float group_max(float m) {
 #pragma unroll
-    for (int off = G / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    for (int off = G / 2; off >= 1; off >>= 1) m = nan_max(m, __shfl_xor(m, off, 64));
     return m;
 }
 
@@ -206,16 +210,17 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
 #pragma unroll
         for (int e = 0; e < 8; e++) {
             v[i][e] *= rs * w[e];
-            amax = fmaxf(amax, fabsf(v[i][e]));
+            amax = nan_max(amax, fabsf(v[i][e]));
         }
         if (g.z) __builtin_nontemporal_store(narrow(v[i]), (u32x4 *)g.z + base + c);
         if constexpr (QB == 128) {
             const float s = group_max<16>(amax) / 448.0f;
             if ((c & 15) == 0) ((float *)g.q_scale)[(base + c) >> 4] = s;
             u32x2 o = {0u, 0u};
-            if (s >= 0x1p-126f) {
+            if (!(s < 0x1p-126f)) {
                 // z * (1/s): z is itself rounded, so a quotient exact to the last bit
-                // would say no more; |z| / s stays below 448.0002
+                // would say no more; |z| / s stays below 448.0002.  A NaN scale gives NaN
+                // codes, an infinite one a NaN code where z is infinite and 0 elsewhere.
                 const float inv = 1.0f / s;
 #pragma unroll
                 for (int e = 0; e < 2; e++)
@@ -236,9 +241,10 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
             const int ef = (int)(bits >> 23);
             int k = (ef - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 7 : 8);
             if (ef == 0 || k < -127) k = -127;
-            if (k > 120) k = 120;   // an infinite amax
-            if ((c & 3) == 0) ((uint8_t *)g.q_scale)[(base + c) >> 2] = m == 0.0f ? 0 : (uint8_t)(k + 127);
-            const float inv = __uint_as_float((uint32_t)(127 - k) << 23);   // 2^-k
+            const bool nan = ef == 255;   // NaN or infinite: E8M0's NaN, and NaN codes
+            if ((c & 3) == 0)
+                ((uint8_t *)g.q_scale)[(base + c) >> 2] = m == 0.0f ? 0 : nan ? 0xFF : (uint8_t)(k + 127);
+            const float inv = nan ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - k) << 23);   // 2^-k
             u32x2 o;
 #pragma unroll
             for (int e = 0; e < 2; e++)

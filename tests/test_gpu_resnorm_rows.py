@@ -1,4 +1,5 @@
-"""resnorm row by row: a row's result is the same in every batch, bit for bit."""
+"""resnorm row by row: a row's result is the same in every batch, bit for bit, and what is
+not finite in it reaches its own results and no other row's."""
 import itertools
 
 import numpy as np
@@ -53,3 +54,83 @@ def test_a_row_does_not_depend_on_its_batch(N):
                 for k, (g, w) in enumerate(zip(got, want)):
                     assert (g is None) == (w is None)
                     assert g is None or same(g, w[lo:hi]), (lo, hi, k)
+
+
+NAN, INF = float("nan"), float("inf")
+SPOILS = [("y", NAN, False), ("y", INF, False), ("y", -INF, True), ("resid", NAN, False), ("resid", INF, True),
+          ("resid", -INF, False), ("gate", NAN, True), ("y_scale", NAN, False), ("code", 0x7F, True)]
+
+
+@pytest.mark.parametrize("N", [512, 1152, 5120])
+@pytest.mark.parametrize("quant", [0, 32, 128])
+def test_what_is_not_finite_stays_visible_and_in_its_row(N, quant):
+    """One value of row 2 is NaN or infinite.  The other rows come out as they do
+    without it.  Row 2 has the formula's NaN in z, a NaN scale and NaN codes in every
+    block with such a z, zeros in the others; and the projection behind gives a
+    row of NaN, its other rows unchanged."""
+    rows, row, col = 7, 2, 300
+    g = torch.Generator(device=device()).manual_seed(N)
+    W = torch.randn((256, N), generator=g, device=device())
+    for what, bad, post in SPOILS:
+        say(f"resnorm not finite: N={N} quant={quant} {what}={bad} post={post}")
+        wire, f32 = what in ("y_scale", "code"), what == "resid"
+        y, r, kw = inputs(rows, N, wire, f32, N + 1)
+        if not post:
+            del kw["post_w"]
+        want = run(y, r, kw, slice(0, rows), quant)
+        y, r, kw = y.clone(), r.clone(), {k: v.clone() if torch.is_tensor(v) else v for k, v in kw.items()}
+        if what == "y_scale":
+            kw["y_scale"][row] = bad
+        else:
+            {"y": y, "code": y, "resid": r, "gate": kw["gate"]}[what][row, col] = bad
+        got = run(y, r, kw, slice(0, rows), quant)
+        torch.cuda.synchronize()
+        others = torch.arange(rows, device=device()) != row
+        for k, (a, b) in enumerate(zip(got, want)):
+            assert (a is None) == (b is None)
+            assert a is None or same(a[others], b[others]), (what, k)
+        # an infinity in h makes 1 / rms 0, so z is NaN where it stands and 0 elsewhere; any
+        # NaN, and an infinity that the norm after the block divides, makes all of it NaN
+        one = np.isinf(bad) and not (what == "y" and post)
+        nan = np.arange(N) == col if one else np.ones(N, bool)
+        z = got[1][row].float().cpu().numpy()
+        assert np.array_equal(np.isnan(z), nan) and not z[~nan].any(), what
+        assert not np.isfinite(got[0][row].float().cpu().numpy()).all()
+        if not quant:
+            continue
+        q, s = got[2][row].cpu().numpy().reshape(-1, quant), got[3][row].cpu().numpy()
+        block = nan.reshape(-1, quant).any(1)
+        assert ((q[block] & 0x7F) == 0x7F).all() and not q[~block].any(), what
+        if quant == 128:
+            assert np.array_equal(np.isnan(s), block) and not s[~block].any(), what
+        else:
+            assert (s[block] == 0xFF).all() and not s[~block].any(), what
+        if quant == 128:
+            B = bs.blockq_e4m3(W, 128)
+            c, c0 = (bs.bsgemm_fp8(t[2], t[3], *B).view(rows, -1) for t in (got, want))
+        else:
+            B = bs.mxq_e4m3(W.to(torch.bfloat16))
+            c, c0 = (bs.mxgemm_fp8(t[2], t[3], *B).view(rows, -1) for t in (got, want))
+        torch.cuda.synchronize()
+        assert bool(c[row].isnan().all()) and same(c[others], c0[others]), what
+
+
+@pytest.mark.parametrize("quant", [32, 128])
+def test_an_infinite_weight_spoils_its_block_alone(quant):
+    """z is infinite in one column: no scale holds it, so its blocks decode to NaN."""
+    say(f"resnorm infinite weight, quant={quant}")
+    rows, N, col = 5, 1152, 700
+    y, r, kw = inputs(rows, N, False, False, 1)
+    want = run(y, r, kw, slice(0, rows), quant)
+    kw["pre_w"] = kw["pre_w"].clone()
+    kw["pre_w"][col] = INF
+    got = run(y, r, kw, slice(0, rows), quant)
+    torch.cuda.synchronize()
+    hit = np.arange(N) // quant == col // quant
+    keep = torch.from_numpy(~hit).to(device())
+    assert bool(got[1][:, col].isinf().all()) and same(got[0], want[0]) and same(got[2][:, keep], want[2][:, keep])
+    s = got[3].cpu().numpy()
+    v = s.astype(float) if quant == 128 else np.where(s == 0xFF, np.nan, 2.0 ** (s.astype(float) - 127))
+    code = got[2].view(torch.float8_e4m3fn).double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        assert np.isnan((code * v.repeat(quant, 1))[:, hit]).all()
