@@ -16,6 +16,7 @@
 // moved once: the kernel is bound by HBM.  16384 wire rows of 7168 with a bf16
 // residual to 1x128 codes: 121 us, 5.8 TB/s; 4096 bf16 rows of 5120 with an fp32
 // residual to bf16 and 1x32 codes: 50 us, 5.5 TB/s; one row of 7168: 4.4 us.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -83,6 +84,33 @@ __device__ __forceinline__ float row_sum(float (&v)[P], float *red) {
     }
 }
 
+// 1 / rms of a row whose squares sum to `sum`.  Where finite values of 2^57 and more
+// take that sum past fp32, the row's values are multiplied by 2^-80 and summed
+// again, and the result is the reciprocal for the smaller values: their normed ones
+// are the same.  Only such rows, and those that are not finite, take the second sum.
+template <int CPT, bool WAVE>
+__device__ __forceinline__ float inv_rms(float sum, float (&v)[CPT][8], int first, const ResnormArgs &g, float *red) {
+    const float inv_n = 1.0f / (float)(g.nch * 8);
+    float eps = g.eps;
+    if (!(sum <= FLT_MAX)) {   // the same for all of the row's lanes
+        float ss[CPT / 2];
+#pragma unroll
+        for (int i = 0; i < CPT; i++) {
+            float sq = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                v[i][e] *= 0x1p-80f;
+                sq += v[i][e] * v[i][e];
+            }
+            if (i % 2 == 0) ss[i / 2] = 0.f;
+            ss[i / 2] += first + 64 * i < g.nch ? sq : 0.f;
+        }
+        sum = row_sum<WAVE>(ss, red);
+        eps = eps * 0x1p-80f * 0x1p-80f;
+    }
+    return 1.0f / sqrtf(sum * inv_n + eps);
+}
+
 // The larger of two values, NaN if either is (fmaxf drops NaN, and a block of
 // NaN would get the scale 0 of a block of zeros).
 __device__ __forceinline__ float nan_max(float a, float b) { return __builtin_elementwise_maximum(a, b); }
@@ -106,13 +134,12 @@ __device__ __forceinline__ float group_max(float m) {
 template <int CPT, bool WAVE, bool WIRE, bool RES32, int QB>
 __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
     constexpr int P = CPT / 2;   // partial sums of squares to a lane
-    __shared__ float red[2][8 * P];
+    __shared__ float red[4][8 * P];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int first = lane + (WAVE ? 0 : wave * 64 * CPT);
     const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
     if (row >= g.rows) return;   // whole waves of a WAVE workgroup
     const int64_t base = row * g.nch;
-    const float inv_n = 1.0f / (float)(g.nch * 8);
 
     u32x4 yw[CPT], ra[CPT], rb[CPT], pw[CPT], gw[CPT], ww[CPT];
     const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};   // bf16 1.0
@@ -161,7 +188,7 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
         }
         ss[i / 2] += live != 0.f ? sq : 0.f;
     }
-    if (g.post_w) mul *= 1.0f / sqrtf(row_sum<WAVE>(ss, red[0]) * inv_n + g.eps);
+    if (g.post_w) mul *= inv_rms<CPT, WAVE>(row_sum<WAVE>(ss, red[0]), v, first, g, red[2]);
 #pragma unroll
     for (int h = 0; h < P; h++) ss[h] = 0.f;
 #pragma unroll
@@ -200,7 +227,7 @@ __global__ void __launch_bounds__(512) resnorm_kernel(ResnormArgs g) {
         }
     }
     if (QB == 0 && !g.z) return;
-    const float rs = 1.0f / sqrtf(row_sum<WAVE>(ss, red[1]) * inv_n + g.eps);
+    const float rs = inv_rms<CPT, WAVE>(row_sum<WAVE>(ss, red[1]), v, first, g, red[3]);
 #pragma unroll
     for (int i = 0; i < CPT; i++) {
         const int c = first + 64 * i;

@@ -440,7 +440,8 @@ bs_status bsgemm_fp8_lora(const uint8_t *A, const float *a_scale, const uint8_t 
  * What is not finite follows the formulas: a NaN or an infinity reaches its own row's
  * z, and a block of z with a NaN gets a NaN scale (byte 0xFF) and NaN codes; one with
  * an infinity gets a scale and codes that decode to NaN (fp32: the scale is infinite;
- * byte 0xFF and NaN codes).
+ * byte 0xFF and NaN codes).  Finite values of any size are normed, those too whose
+ * squares are past fp32; only h itself has to lie within it.
  *
  *   y          bf16 [rows, N], or e4m3 [rows, N] with y_scale fp32 [rows]
  *   resid      bf16 [rows, N], or fp32 if resid_f32 is 1; resid_out the same
@@ -450,7 +451,6 @@ bs_status bsgemm_fp8_lora(const uint8_t *A, const float *a_scale, const uint8_t 
  *   z          bf16 [rows, N] or null
  *   q, q_scale e4m3 [rows, N] with fp32 [rows, N/128] or bytes [rows, N/32];
  *              both null if q_block is 0
- *   (squares that sum past fp32's range count as infinite)
  *
  * Requirements: 0 <= rows < 2^31; N > 0, N % 8 == 0 (N % q_block == 0 with
  * q), N <= 16384; eps > 0 and alpha, beta, eps finite; every pointer 16-byte

@@ -7,7 +7,9 @@ import pytest
 import torch
 
 import block_scaled_fp8_bsgemm_amd as bs
-from gpuutil import device, say
+import opsref
+from gpuutil import bits16, device, say
+from oracle import bounds
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +136,54 @@ def test_an_infinite_weight_spoils_its_block_alone(quant):
     code = got[2].view(torch.float8_e4m3fn).double().cpu().numpy()
     with np.errstate(invalid="ignore"):
         assert np.isnan((code * v.repeat(quant, 1))[:, hit]).all()
+
+
+def values(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def large(what, N, f32):
+    """Eight rows, of which every second one has values whose squares, or their sum,
+    lie past fp32."""
+    wire = what == "y_scale"
+    y, r, kw = inputs(8, N, wire, f32, N + 2)
+    kw["gate"] = kw["gate"].clamp(-4, 4)
+    if what == "y":                      # the largest bf16 among them
+        y[1::2] *= 2.0 ** 120
+        y[3] = y[3].sign() * torch.finfo(torch.bfloat16).max
+    elif what == "y_scale":
+        kw["y_scale"][1::2] = 2.0 ** 100
+    elif what == "border":               # the sum of squares just past fp32 and just below it
+        y.zero_()
+        r[1::2] = 2.0 ** 64 / N ** 0.5 * 1.02
+        r[0::2] = 2.0 ** 64 / N ** 0.5 * 0.98
+        kw["alpha"] = 1.0
+    elif what == "one":                  # a single one in its row
+        r[1::2, 77] = 2.0 ** 100
+    else:
+        r[1::2] *= 2.0 ** 110
+    return y, r, kw, wire
+
+
+@pytest.mark.parametrize("N", [512, 1152, 8192])
+@pytest.mark.parametrize("what", ["y", "y_scale", "resid", "one", "border"])
+def test_squares_past_fp32(what, N):
+    """Held to the same bounds as rows of ordinary size: the powers of two in between
+    are exact."""
+    for f32, quant in itertools.product((False, True), (0, 32, 128)):
+        say(f"resnorm squares past fp32: {what} N={N} f32={f32} quant={quant}")
+        y, r, kw, wire = large(what, N, f32)
+        got = run(y, r, kw, slice(0, 8), quant)
+        torch.cuda.synchronize()
+        yv = values(y.view(torch.float8_e4m3fn)) * values(kw["y_scale"])[:, None] if wire else values(y)
+        h, eh, z, ez = opsref.resnorm(yv, values(r), values(kw["post_w"]), values(kw["gate"]), values(kw["pre_w"]),
+                                      kw["alpha"], kw["beta"], 1e-6)
+        assert np.isfinite(values(got[0])).all() and np.isfinite(values(got[1])).all()
+        if f32:
+            assert np.all(np.abs(values(got[0]) - h) <= eh + opsref.U * np.abs(h))
+        else:
+            assert bounds.within(bits16(got[0]), h, eh)[0].all()
+        assert bounds.within(bits16(got[1]), z, ez)[0].all()
+        if quant:
+            s = values(got[3]) if quant == 128 else 2.0 ** (got[3].cpu().numpy() - 127.0)
+            opsref.check_quant(got[2].cpu().numpy(), s, z, ez, quant)
