@@ -301,16 +301,38 @@ int launch_t(const ResnormArgs &g, bool resid_f32, int q_block, hipStream_t stre
                      : launch_q<CPT, WAVE, false, false>(g, q_block, grid, block, stream);
 }
 
+// The call's rows from `first` on, `rows` of them at most.
+ResnormArgs rows_from(ResnormArgs g, int64_t first, int64_t rows, bool resid_f32, int q_block) {
+    const int64_t at = first * g.nch * 8;
+    g.y = (const uint8_t *)g.y + at * (g.y_scale ? 1 : 2);
+    if (g.y_scale) g.y_scale += first;
+    if (g.gate) g.gate += first * g.gate_row;
+    g.resid = (const uint8_t *)g.resid + at * (resid_f32 ? 4 : 2);
+    g.resid_out = (uint8_t *)g.resid_out + at * (resid_f32 ? 4 : 2);
+    if (g.z) g.z += at;
+    if (g.q) g.q += at;
+    if (q_block) g.q_scale = (uint8_t *)g.q_scale + at / 32;   // n / 128 fp32, or n / 32 bytes
+    g.rows = g.rows - first < rows ? g.rows - first : rows;
+    return g;
+}
+
 }  // namespace
 
-int bs_launch_resnorm(const ResnormArgs &g, bool resid_f32, int q_block, hipStream_t stream) {
-    if (g.rows > 0x7FFFFFFF) return -1;
-    // a row has as few lanes as hold it in CPT packs each, so that few are idle
-    // (N = 7168: 7 waves of 2 packs, or 4 of 4).  Few rows want the shorter chain
-    // of 2 packs, many the fewer waves to join: graph launches of wire rows to
-    // codes at N = 7168, 2 packs / 4: 1 row 4.8 / 5.5 us, 64 rows 4.6 / 5.4, 16384
-    // rows 130 / 126; 2512 bf16 rows of 1536 to bf16: 10.1 / 8.9.
-    if (g.nch <= 128) return launch_t<2, true>(g, resid_f32, q_block, stream);
-    if (g.nch <= 1024 && g.rows < 512) return launch_t<2, false>(g, resid_f32, q_block, stream);
-    return launch_t<4, false>(g, resid_f32, q_block, stream);
+int bs_launch_resnorm(const ResnormArgs &all, bool resid_f32, int q_block, hipStream_t stream) {
+    // A launch holds fewer than 2^32 lanes, and a row has at most 512: more rows than
+    // 2^22 go in several launches.
+    constexpr int64_t ROWS = (int64_t)1 << 22;
+    for (int64_t first = 0; first < all.rows; first += ROWS) {
+        const ResnormArgs g = rows_from(all, first, ROWS, resid_f32, q_block);
+        // a row has as few lanes as hold it in CPT packs each, so that few are idle
+        // (N = 7168: 7 waves of 2 packs, or 4 of 4).  Few rows want the shorter chain
+        // of 2 packs, many the fewer waves to join: graph launches of wire rows to
+        // codes at N = 7168, 2 packs / 4: 1 row 4.8 / 5.5 us, 64 rows 4.6 / 5.4, 16384
+        // rows 130 / 126; 2512 bf16 rows of 1536 to bf16: 10.1 / 8.9.
+        const int rc = g.nch <= 128                       ? launch_t<2, true>(g, resid_f32, q_block, stream)
+                       : g.nch <= 1024 && all.rows < 512 ? launch_t<2, false>(g, resid_f32, q_block, stream)
+                                                          : launch_t<4, false>(g, resid_f32, q_block, stream);
+        if (rc != 0) return rc;
+    }
+    return 0;
 }

@@ -1,0 +1,49 @@
+"""Batches of more rows than one launch of a workgroup a row, or a row tile, may
+hold (2^32 lanes a launch): short rows, a few of them compared with the same
+rows in a small batch, bit for bit, or with exact integers."""
+import pytest
+import torch
+
+import block_scaled_fp8_bsgemm_amd as bs
+from gpuutil import device, say
+
+pytestmark = pytest.mark.gpu
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("N,quant", [(8, 0), (32, 32), (128, 128)])
+def test_resnorm_rows(N, quant):
+    """Rows around every 2^22nd are filled; the rest are zeros and come out so."""
+    rows = (1 << 26) + 37
+    say(f"resnorm rows={rows} N={N} quant={quant}")
+    d = device()
+    g = torch.Generator(device=d).manual_seed(N)
+    edge = torch.arange(0, rows, 1 << 22, device=d)
+    at = torch.unique(torch.cat([edge, (edge - 1).clamp_min(0), torch.arange(rows - 40, rows, device=d)]))
+    y = torch.zeros((rows, N), dtype=torch.uint8, device=d)
+    y[at] = torch.randint(0, 0x7F, (len(at), N), generator=g, device=d, dtype=torch.uint8)
+    s = torch.zeros(rows, device=d)
+    s[at] = torch.rand(len(at), generator=g, device=d)
+    r = torch.zeros((rows, N), dtype=torch.bfloat16, device=d)
+    r[at] = torch.randn((len(at), N), generator=g, device=d).to(torch.bfloat16)
+    w = torch.randn(N, generator=g, device=d).to(torch.bfloat16)
+    want = bs.resnorm(y[at], r[at], y_scale=s[at], post_w=w, gate=w, quant=quant)
+    got = bs.resnorm(y, r, y_scale=s, post_w=w, gate=w, quant=quant)
+    torch.cuda.synchronize()
+    for k, (a, b) in enumerate(zip(got, want)):
+        assert (a is None) == (b is None)
+        if a is not None:
+            assert same(a.view(rows, -1)[at], b.view(len(at), -1)), k
+            a.view(rows, -1)[at] = 0
+            assert int(a.count_nonzero()) == 0, k
+    if quant:
+        return
+    # a gate row for each row, in place
+    gate = torch.zeros((rows, N), dtype=torch.bfloat16, device=d)
+    gate[at] = w
+    bs.resnorm(y, r, y_scale=s, post_w=w, gate=gate, resid_out=r, z=got[1])
+    torch.cuda.synchronize()
+    assert same(r[at], want[0]) and same(got[1][at], want[1])
