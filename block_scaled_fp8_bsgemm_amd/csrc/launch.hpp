@@ -71,7 +71,9 @@ int bs_launch_resnorm(const ResnormArgs &g, bool resid_f32, int q_block, hipStre
 #include <tuple>
 
 // Enqueue `kernel` with hipLaunchKernel and report that launch's own status
-// (not a sticky error left by an unrelated earlier call).
+// (not a sticky error left by an unrelated earlier call).  No dimension may hold 2^32
+// lanes or more: the runtime refuses that or, seen too, runs their number modulo
+// 2^32 and reports success.
 template <typename... KArgs, typename... Args>
 int bs_enqueue(void (*kernel)(KArgs...), dim3 grid, dim3 block, hipStream_t stream, Args... args) {
     static_assert(sizeof...(KArgs) == sizeof...(Args), "kernel argument count");

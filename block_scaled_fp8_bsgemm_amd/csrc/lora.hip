@@ -143,6 +143,12 @@ __device__ __forceinline__ RowTile find_tile(const int32_t *plan, int M, int L, 
 // The most tiles that M rows in L + 1 groups can make.
 inline int64_t max_tiles(int64_t M, int64_t L, int T) { return M / T + (L + 1 < M ? L + 1 : M); }
 
+// Workgroups of at most 512 lanes in a grid of x by y (or z) of them: a launch
+// holds fewer than 2^32 lanes along x, which the tiles of 2^29 rows pass.
+constexpr int64_t GRID_X = (int64_t)1 << 22;
+inline unsigned grid_x(int64_t n) { return (unsigned)(n < GRID_X ? n : GRID_X); }
+inline unsigned grid_more(int64_t n) { return (unsigned)((n + GRID_X - 1) / GRID_X); }
+
 // The batch row of the tile's row `lane`, one load for the wave; M (no row) past
 // the tile's count or for an entry that is no row.  Any lane's is then had by a
 // shuffle.
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(W * 64) lora_shrink_kernel(ShrinkArgs g) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fg = lane >> 4;
-    const RowTile t = find_tile<16 * RT>(g.plan, g.M, g.L, blockIdx.x, lane);
+    const RowTile t = find_tile<16 * RT>(g.plan, g.M, g.L, blockIdx.z * GRID_X + blockIdx.x, lane);
     if (t.count <= 0) return;
     const int32_t *order = g.plan + g.L + 2;
     const int c0 = blockIdx.y * 16 * CT;
@@ -294,7 +300,8 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(ExpandArgs g) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fg = lane >> 4;
-    const int tile = (int)(blockIdx.x / (unsigned)g.col_blocks);
+    const unsigned wg = blockIdx.y * (unsigned)GRID_X + blockIdx.x;
+    const int tile = (int)(wg / (unsigned)g.col_blocks);
     const RowTile t = find_tile<16 * RT>(g.plan, g.M, g.lora.L, tile, lane);
     if (t.count <= 0) return;
     const bool has = t.group < g.lora.L;
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(ExpandArgs g) {
             const int64_t gap = g.band_gap ? g.band_gap * ((uint32_t)m / (uint32_t)g.band_rows) : 0;
             at[i][h] = m < g.M ? m * g.N + gap : -1;
         }
-    const int64_t first = (int64_t)((int)blockIdx.x - tile * g.col_blocks) * g.chunks;
+    const int64_t first = (int64_t)((int)wg - tile * g.col_blocks) * g.chunks;
     const int64_t end = min((first + g.chunks) * 256, g.N);
     const int dx = 8 * fg + (up ? 32 : 0), dy = 8 * fg + (up ? 0 : 32);
     const int64_t c0 = first * 256;
@@ -410,7 +417,8 @@ int bs_launch_lora_plan(const int32_t *ids, int32_t *plan, int64_t M, int L, hip
 template <int RT, int CT, int UN>
 static int launch_shrink(const ShrinkArgs &g, hipStream_t stream) {
     constexpr int W = 8;
-    const dim3 grid((unsigned)max_tiles(g.M, g.L, 16 * RT), (unsigned)((g.R + 16 * CT - 1) / (16 * CT)));
+    const int64_t tiles = max_tiles(g.M, g.L, 16 * RT);
+    const dim3 grid(grid_x(tiles), (unsigned)((g.R + 16 * CT - 1) / (16 * CT)), grid_more(tiles));
     return bs_enqueue(lora_shrink_kernel<RT, CT, W, UN>, grid, dim3(64 * W), stream, g);
 }
 
@@ -443,8 +451,9 @@ static int launch_expand(ExpandArgs g, hipStream_t stream) {
     if (chunks > 4096) chunks = 4096;   // offsets within a workgroup's part of B: below 2^30
     g.chunks = (int)chunks;
     g.col_blocks = (int)((cols + chunks - 1) / chunks);
-    if (tiles * g.col_blocks > 0x7FFFFFFF) return -1;
-    return bs_enqueue(lora_expand_kernel<RT, RMAX>, dim3((unsigned)(tiles * g.col_blocks)), dim3(256), stream, g);
+    const int64_t n = tiles * g.col_blocks;
+    if (n > 0x7FFFFFFF) return -1;
+    return bs_enqueue(lora_expand_kernel<RT, RMAX>, dim3(grid_x(n), grid_more(n)), dim3(256), stream, g);
 }
 
 template <int RT>

@@ -47,3 +47,49 @@ def test_resnorm_rows(N, quant):
     bs.resnorm(y, r, y_scale=s, post_w=w, gate=gate, resid_out=r, z=got[1])
     torch.cuda.synchronize()
     assert same(r[at], want[0]) and same(got[1][at], want[1])
+
+
+def thirds(M):
+    """ids -1, 0, 1, -1, ... and the plan of two adapters for them, checked."""
+    d = device()
+    ids = torch.arange(M, dtype=torch.int32, device=d) % 3 - 1
+    plan = bs.lora_plan(ids, 2)
+    n = [(M - r + 2) // 3 for r in (1, 2, 0)]   # rows of adapter 0, of 1, and without
+    assert plan[:4].tolist() == [0, n[0], n[0] + n[1], M]
+    at = 4
+    for r, k in zip((1, 2, 0), n):
+        assert torch.equal(plan[at:at + k], torch.arange(r, M, 3, dtype=torch.int32, device=d))
+        at += k
+    return ids, plan
+
+
+def check_rows(t, ids, table):
+    """Each row of t is its adapter's row of table (the last one without)."""
+    for i in range(0, len(t), 1 << 22):
+        assert torch.equal(t[i:i + (1 << 22)], table[ids[i:i + (1 << 22)].long()]), i
+
+
+def test_shrink_rows():
+    M, K, R = (1 << 29) + 70, 8, 8
+    say(f"lora_plan, lora_shrink M={M}")
+    d = device()
+    ids, plan = thirds(M)
+    x = torch.ones((M, K), dtype=torch.bfloat16, device=d)
+    A = torch.randint(-3, 4, (2, R, K), generator=torch.Generator(device=d).manual_seed(0), device=d)
+    H = torch.full((M, R), float("nan"), device=d)
+    bs.lora_shrink(x, A.to(torch.bfloat16), plan, H)
+    torch.cuda.synchronize()
+    check_rows(H, ids, torch.cat([A.float().sum(2), torch.zeros((1, R), device=d)]))
+
+
+def test_expand_rows():
+    M, N, R = (1 << 30) - 1, 8, 8
+    say(f"lora_plan, lora_expand M={M}, in place")
+    d = device()
+    ids, plan = thirds(M)
+    H = torch.ones((M, R), device=d)
+    B = torch.randint(-3, 4, (2, N, R), generator=torch.Generator(device=d).manual_seed(1), device=d)
+    out = torch.ones((M, N), dtype=torch.bfloat16, device=d)
+    bs.lora_expand(H, B.to(torch.bfloat16), plan, out, out)
+    torch.cuda.synchronize()
+    check_rows(out, ids, 1 + torch.cat([B.sum(2), torch.zeros((1, N), device=d, dtype=B.dtype)]).to(torch.bfloat16))
