@@ -515,19 +515,25 @@ int bs_launch_rowq(const uint16_t *x, uint8_t *q, float *scale, int64_t rows, in
         const dim3 grid(grid_rows(rows)), block(256);
         return bs_enqueue(rowq_long_kernel, grid, block, stream, xv, qv, scale, rows, nch);
     }
-    const int64_t wg = (rows + 3) / 4;
-    if (wg > 0x7FFFFFFF) return -1;
-    const dim3 grid((unsigned)wg), block(256);
-    if (nch <= 256)
-        rc |= launch_rowq<4>(grid, block, stream, xv, qv, scale, rows, nch);
-    else if (nch <= 512)
-        rc |= launch_rowq<8>(grid, block, stream, xv, qv, scale, rows, nch);
-    else if (nch <= 896)
-        rc |= launch_rowq<14>(grid, block, stream, xv, qv, scale, rows, nch);
-    else if (nch <= 1024)
-        rc |= launch_rowq<16>(grid, block, stream, xv, qv, scale, rows, nch);
-    else
-        rc |= launch_rowq<32>(grid, block, stream, xv, qv, scale, rows, nch);
+    // four rows of a wavefront each to a workgroup; a launch holds fewer than 2^32 lanes
+    constexpr int64_t ROWS = (int64_t)1 << 24;
+    for (int64_t r = 0; r < rows && rc == 0; r += ROWS) {
+        const int64_t n = rows - r < ROWS ? rows - r : ROWS;
+        const u32x4 *xr = xv + r * nch;
+        u32x2 *qr = qv + r * nch;
+        float *sr = scale + r;
+        const dim3 grid((unsigned)((n + 3) / 4)), block(256);
+        if (nch <= 256)
+            rc = launch_rowq<4>(grid, block, stream, xr, qr, sr, n, nch);
+        else if (nch <= 512)
+            rc = launch_rowq<8>(grid, block, stream, xr, qr, sr, n, nch);
+        else if (nch <= 896)
+            rc = launch_rowq<14>(grid, block, stream, xr, qr, sr, n, nch);
+        else if (nch <= 1024)
+            rc = launch_rowq<16>(grid, block, stream, xr, qr, sr, n, nch);
+        else
+            rc = launch_rowq<32>(grid, block, stream, xr, qr, sr, n, nch);
+    }
     return rc;
 }
 
@@ -550,12 +556,16 @@ int bs_launch_rowdq(const uint8_t *q, const float *scale, uint16_t *y, int64_t r
 int bs_launch_blockq(const float *x, uint8_t *q, float *scale, int64_t rows, int64_t cols,
                      int block_rows, hipStream_t stream) {
     if (block_rows == 1) {
+        // 16 lanes to a block; a launch holds fewer than 2^32
+        constexpr int64_t BLOCKS = (int64_t)1 << 27;
         const int64_t nblocks = rows * (cols / 128);
-        const int64_t threads = nblocks * 16;
-        const int64_t wg = (threads + 255) / 256;
-        if (wg > 0x7FFFFFFF) return -1;
-        return bs_enqueue(blockq_1x128_kernel, dim3((unsigned)(wg > 0 ? wg : 1)), dim3(256), stream,
-                          (const u32x4 *)x, (u32x2 *)q, scale, nblocks);
+        int rc = 0;
+        for (int64_t b = 0; b < nblocks && rc == 0; b += BLOCKS) {
+            const int64_t n = nblocks - b < BLOCKS ? nblocks - b : BLOCKS;
+            rc = bs_enqueue(blockq_1x128_kernel, dim3((unsigned)((n * 16 + 255) / 256)), dim3(256), stream,
+                            (const u32x4 *)(x + b * 128), (u32x2 *)(q + b * 128), scale + b, n);
+        }
+        return rc;
     }
     const int64_t nb = ((rows + 127) / 128) * (cols / 128);
     if (nb > 0x7FFFFFFF) return -1;
@@ -585,13 +595,19 @@ int bs_launch_mxq(const uint16_t *x, uint8_t *q, uint8_t *e, int64_t rows, int64
 
 int bs_launch_band_rowq(const uint16_t *const *parts, int P, uint8_t *q, float *scale, int64_t rows,
                         int64_t N, hipStream_t stream) {
-    PartPtrs pp;
-    for (int p = 0; p < 16; p++) pp.p[p] = (const u32x4 *)parts[p < P ? p : 0];
     const int nch = (int)(N / 8);
-    if (rows > 0x7FFFFFFF || nch > 256 * BRQ_CPT) return -1;
+    if (nch > 256 * BRQ_CPT) return -1;
     // parts per load group: 4 measured fastest at P = 8, [2048, 7168]
     // (42.2 us against 43.7 for 2 and 43.1 for 8)
     constexpr int G = 4;
-    return bs_enqueue(band_rowq_kernel<G>, dim3((unsigned)rows), dim3(256), stream, pp, P,
-                      (u32x2 *)q, scale, nch);
+    // a workgroup to a row; a launch holds fewer than 2^32 lanes
+    constexpr int64_t ROWS = (int64_t)1 << 23;
+    int rc = 0;
+    for (int64_t r = 0; r < rows && rc == 0; r += ROWS) {
+        PartPtrs pp;
+        for (int p = 0; p < 16; p++) pp.p[p] = (const u32x4 *)parts[p < P ? p : 0] + r * nch;
+        rc = bs_enqueue(band_rowq_kernel<G>, dim3((unsigned)(rows - r < ROWS ? rows - r : ROWS)), dim3(256), stream, pp,
+                        P, (u32x2 *)(q + r * N), scale + r, nch);
+    }
+    return rc;
 }

@@ -93,3 +93,33 @@ def test_expand_rows():
     bs.lora_expand(H, B.to(torch.bfloat16), plan, out, out)
     torch.cuda.synchronize()
     check_rows(out, ids, 1 + torch.cat([B.sum(2), torch.zeros((1, N), device=d, dtype=B.dtype)]).to(torch.bfloat16))
+
+
+def edges(rows, step):
+    """Row numbers on either side of every step-th, and the last ones."""
+    edge = torch.arange(0, rows, step, device=device())
+    return torch.unique(torch.cat([edge, (edge - 1).clamp_min(0), torch.arange(rows - 40, rows, device=device())]))
+
+
+@pytest.mark.parametrize("call,rows,N", [("rowq_e4m3", (1 << 26) + 37, 8), ("band_rowq_e4m3", (1 << 24) + 37, 8),
+                                         ("blockq_e4m3", (1 << 28) + 37, 128)])
+def test_quantizer_rows(call, rows, N):
+    """The filled rows' codes and scales against a small batch's, zeros elsewhere."""
+    say(f"{call} rows={rows} N={N}")
+    d, block = device(), call == "blockq_e4m3"
+    fn = {"rowq_e4m3": bs.rowq_e4m3, "band_rowq_e4m3": lambda x, *o: bs.band_rowq_e4m3([x, x.clone()], *o),
+          "blockq_e4m3": lambda x, *o: bs.blockq_e4m3(x, 1, *o)}[call]
+    at = edges(rows, 1 << 22)
+    few = torch.randn((len(at), N), generator=torch.Generator(device=d).manual_seed(N), device=d)
+    few = few if block else few.to(torch.bfloat16)
+    x = torch.zeros((rows, N), dtype=few.dtype, device=d)
+    x[at] = few
+    q = torch.full((rows, N), 0x7F, dtype=torch.uint8, device=d)
+    s = torch.full((rows, 1), -3.0, device=d)
+    fn(x, q, s)
+    want = fn(few)
+    torch.cuda.synchronize()
+    for got, w in zip((q, s), want):
+        assert same(got[at], w.view(len(at), -1))
+        got[at] = 0
+        assert all(int(part.count_nonzero()) == 0 for part in got.split(1 << 24))
