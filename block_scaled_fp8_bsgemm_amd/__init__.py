@@ -28,6 +28,8 @@ library has not been built, importing the functions raises immediately.
 Tensors: e4m3 codes are uint8 (or torch.float8_e4m3fn, reinterpreted), bf16
 values are torch.bfloat16 (or int16/uint16 bit patterns), scales float32.
 All tensors must live on the current CUDA (HIP) device and be contiguous.
+Every call takes stream=None, the torch.cuda.Stream to enqueue on (None: the
+current one); outputs that it allocates belong to that stream.
 The C ABI receives raw pointers and cannot see sizes, so every wrapper checks
 each operand's shape and each output's element count against the sizes the
 call implies before it takes a pointer, and raises ValueError on a mismatch:
@@ -167,6 +169,16 @@ def _stream(stream=None):
     return s.cuda_stream
 
 
+def _empty(stream, shape, dtype, device):
+    """An output of the call, allocated for the stream that writes it: the memory that a
+    tensor of the current stream has left may still be in use there."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _u8():
     torch = _torch()
     return (torch.uint8, torch.int8, torch.float8_e4m3fn)
@@ -188,7 +200,7 @@ def bsgemm_fp8(A, a_scale, B, b_scale, C=None, bands=1, band_stride=0, stream=No
     M, N, K = _check_gemm_operands(A, a_scale, B, b_scale, 128, "bsgemm_fp8")
     need = _band_elems(M, N, bands, band_stride)
     if C is None:
-        C = torch.empty(need, dtype=torch.bfloat16, device=A.device)
+        C = _empty(stream, need, dtype=torch.bfloat16, device=A.device)
     _room(C, need, "C")
     st = load().bsgemm_fp8(_ptr(A, _u8(), "A"), _ptr(a_scale, _f32(), "a_scale"),
                            _ptr(B, _u8(), "B"), _ptr(b_scale, _f32(), "b_scale"),
@@ -206,7 +218,7 @@ def band_reduce(parts, out=None, stream=None):
     for i, p in enumerate(parts):
         _shape(p, (rows, N), f"parts[{i}]")
     if out is None:
-        out = torch.empty((rows, N), dtype=torch.bfloat16, device=parts[0].device)
+        out = _empty(stream, (rows, N), dtype=torch.bfloat16, device=parts[0].device)
     _room(out, rows * N, "out")
     ptrs = (ctypes.c_void_p * len(parts))(*[_ptr(p, _b16(), "part") for p in parts])
     st = load().band_reduce(ptrs, len(parts), _ptr(out, _b16(), "out"), rows, N, _stream(stream))
@@ -219,9 +231,9 @@ def rowq_e4m3(x, q=None, scale=None, stream=None):
     torch = _torch()
     rows, N = _dims2(x, "x")
     if q is None:
-        q = torch.empty((rows, N), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (rows, N), dtype=torch.uint8, device=x.device)
     if scale is None:
-        scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        scale = _empty(stream, (rows,), dtype=torch.float32, device=x.device)
     _room(q, rows * N, "q")
     _room(scale, rows, "scale")
     st = load().rowq_e4m3(_ptr(x, _b16(), "x"), _ptr(q, _u8(), "q"), _ptr(scale, _f32(), "scale"),
@@ -236,7 +248,7 @@ def rowdq_e4m3(q, scale, y=None, stream=None):
     rows, N = _dims2(q, "q")
     _need(scale.numel() == rows, f"scale: {scale.numel()} elements for {rows} rows")
     if y is None:
-        y = torch.empty((rows, N), dtype=torch.bfloat16, device=q.device)
+        y = _empty(stream, (rows, N), dtype=torch.bfloat16, device=q.device)
     _room(y, rows * N, "y")
     st = load().rowdq_e4m3(_ptr(q, _u8(), "q"), _ptr(scale, _f32(), "scale"), _ptr(y, _b16(), "y"),
                            rows, N, _stream(stream))
@@ -251,10 +263,10 @@ def blockq_e4m3(x, block_rows, q=None, scale=None, stream=None):
     _need(block_rows in (1, 128), f"blockq_e4m3: block_rows must be 1 or 128, got {block_rows}")
     nscale = ((rows + block_rows - 1) // block_rows) * (cols // 128)
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (rows, cols), dtype=torch.uint8, device=x.device)
     if scale is None:
-        scale = torch.empty(((rows + block_rows - 1) // block_rows, cols // 128), dtype=torch.float32,
-                            device=x.device)
+        scale = _empty(stream, ((rows + block_rows - 1) // block_rows, cols // 128), dtype=torch.float32,
+                       device=x.device)
     _room(q, rows * cols, "q")
     _room(scale, nscale, "scale")
     st = load().blockq_e4m3(_ptr(x, _f32(), "x"), _ptr(q, _u8(), "q"), _ptr(scale, _f32(), "scale"),
@@ -268,9 +280,9 @@ def actq_e4m3(x, q=None, scale=None, stream=None):
     torch = _torch()
     rows, cols = _dims2(x, "x")
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (rows, cols), dtype=torch.uint8, device=x.device)
     if scale is None:
-        scale = torch.empty((rows, cols // 128), dtype=torch.float32, device=x.device)
+        scale = _empty(stream, (rows, cols // 128), dtype=torch.float32, device=x.device)
     _room(q, rows * cols, "q")
     _room(scale, rows * (cols // 128), "scale")
     st = load().actq_e4m3(_ptr(x, _b16(), "x"), _ptr(q, _u8(), "q"), _ptr(scale, _f32(), "scale"),
@@ -286,7 +298,7 @@ def mxgemm_fp8(A, a_scale, B, b_scale, C=None, bands=1, band_stride=0, stream=No
     M, N, K = _check_gemm_operands(A, a_scale, B, b_scale, 32, "mxgemm_fp8")
     need = _band_elems(M, N, bands, band_stride)
     if C is None:
-        C = torch.empty(need, dtype=torch.bfloat16, device=A.device)
+        C = _empty(stream, need, dtype=torch.bfloat16, device=A.device)
     _room(C, need, "C")
     st = load().mxgemm_fp8(_ptr(A, _u8(), "A"), _ptr(a_scale, _u8(), "a_scale"),
                            _ptr(B, _u8(), "B"), _ptr(b_scale, _u8(), "b_scale"),
@@ -300,9 +312,9 @@ def mxq_e4m3(x, q=None, scale=None, stream=None):
     torch = _torch()
     rows, cols = _dims2(x, "x")
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (rows, cols), dtype=torch.uint8, device=x.device)
     if scale is None:
-        scale = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
+        scale = _empty(stream, (rows, cols // 32), dtype=torch.uint8, device=x.device)
     _room(q, rows * cols, "q")
     _room(scale, rows * (cols // 32), "scale")
     st = load().mxq_e4m3(_ptr(x, _b16(), "x"), _ptr(q, _u8(), "q"), _ptr(scale, _u8(), "scale"),
@@ -316,7 +328,7 @@ def bprepack_e4m3(B, Bp=None, stream=None):
     torch = _torch()
     N, K = _dims2(B, "B")
     if Bp is None:
-        Bp = torch.empty(N * K, dtype=torch.uint8, device=B.device)
+        Bp = _empty(stream, N * K, dtype=torch.uint8, device=B.device)
     _room(Bp, N * K, "Bp")
     st = load().bprepack_e4m3(_ptr(B, _u8(), "B"), _ptr(Bp, _u8(), "Bp"), N, K, _stream(stream))
     _check(st, "bprepack_e4m3")
@@ -336,7 +348,7 @@ def bsgemm_fp8_pb(A, a_scale, Bp, b_scale, C=None, bands=1, band_stride=0, strea
     _need(Bp.numel() == N * K, f"Bp must hold N*K = {N * K} bytes, got {Bp.numel()}")
     need = _band_elems(M, N, bands, band_stride)
     if C is None:
-        C = torch.empty(need, dtype=torch.bfloat16, device=A.device)
+        C = _empty(stream, need, dtype=torch.bfloat16, device=A.device)
     _room(C, need, "C")
     st = load().bsgemm_fp8_pb(_ptr(A, _u8(), "A"), _ptr(a_scale, _f32(), "a_scale"),
                               _ptr(Bp, _u8(), "Bp"), _ptr(b_scale, _f32(), "b_scale"),
@@ -354,9 +366,9 @@ def band_rowq_e4m3(parts, q=None, scale=None, stream=None):
     for i, p in enumerate(parts):
         _shape(p, (rows, N), f"parts[{i}]")
     if q is None:
-        q = torch.empty((rows, N), dtype=torch.uint8, device=parts[0].device)
+        q = _empty(stream, (rows, N), dtype=torch.uint8, device=parts[0].device)
     if scale is None:
-        scale = torch.empty((rows,), dtype=torch.float32, device=parts[0].device)
+        scale = _empty(stream, (rows,), dtype=torch.float32, device=parts[0].device)
     _room(q, rows * N, "q")
     _room(scale, rows, "scale")
     ptrs = (ctypes.c_void_p * len(parts))(*[_ptr(p, _b16(), "part") for p in parts])
@@ -455,7 +467,7 @@ def lora_plan(ids, n_adapters, plan=None, stream=None):
         raise ValueError(f"lora_plan: n_adapters must be at least 1, got {n_adapters}")
     M = ids.shape[0]
     if plan is None:
-        plan = ty.torch.empty(n_adapters + 2 + M, dtype=ty.torch.int32, device=ids.device)
+        plan = _empty(stream, n_adapters + 2 + M, dtype=ty.torch.int32, device=ids.device)
     _check_plan(plan, M, n_adapters)
     p, st = _args("lora_plan", stream, (ids, ty.i32, "ids"), (plan, ty.i32, "plan"))
     _check(load().lora_plan(*p, M, n_adapters, st), "lora_plan")
@@ -472,7 +484,7 @@ def lora_shrink(x, A, plan, H=None, stream=None):
     L, R, _ = A.shape
     _check_plan(plan, M, L)
     if H is None:
-        H = ty.torch.empty((M, R), dtype=ty.torch.float32, device=x.device)
+        H = _empty(stream, (M, R), dtype=ty.torch.float32, device=x.device)
     _fits(H, M * R, "H")
     p, st = _args("lora_shrink", stream, (x, ty.bf, "x"), (A, ty.bf, "A"), (plan, ty.i32, "plan"), (H, ty.f32, "H"))
     if M:
@@ -502,7 +514,7 @@ def lora_expand(H, B, plan, base, out=None, scale=None, bands=1, band_stride=0, 
     if not (base.numel() >= need):
         raise ValueError(f"base: {base.numel()} elements, the call reads {need}")
     if out is None:
-        out = ty.torch.empty(need, dtype=ty.torch.bfloat16, device=base.device)
+        out = _empty(stream, need, dtype=ty.torch.bfloat16, device=base.device)
     _fits(out, need, "out")
     p, st = _args("lora_expand", stream, (H, ty.f32, "H"), (B, ty.bf, "B"), (scale, ty.f32, "scale"),
                   (plan, ty.i32, "plan"), (base, ty.bf, "base"), (out, ty.bf, "out"))
@@ -528,7 +540,7 @@ def bsgemm_fp8_lora(A, a_scale, B, b_scale, H, lora_B, ids, scale=None, C=None, 
     _is(ids, (M,), "ids")
     need = _band_elems(M, N, bands, band_stride)
     if C is None:
-        C = ty.torch.empty(need, dtype=ty.torch.bfloat16, device=A.device)
+        C = _empty(stream, need, dtype=ty.torch.bfloat16, device=A.device)
     _fits(C, need, "C")
     p, st = _args("bsgemm_fp8_lora", stream, (A, ty.u8, "A"), (a_scale, ty.f32, "a_scale"), (B, ty.u8, "B"),
                   (b_scale, ty.f32, "b_scale"), (H, ty.f32, "H"), (lora_B, ty.bf, "lora_B"), (scale, ty.f32, "scale"),
@@ -565,7 +577,7 @@ def resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.
         gate_row = N if gate.dim() == 2 else 0
         _is(gate, (rows, N) if gate_row else (N,), "gate")
     if resid_out is None:
-        resid_out = torch.empty_like(resid)
+        resid_out = _empty(stream, (rows, N), resid.dtype, resid.device)
     elif resid_out.dtype != resid.dtype:
         raise ValueError(f"resid_out is {resid_out.dtype}, resid is {resid.dtype}")
     n = rows * N
@@ -574,17 +586,17 @@ def resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.
         if N % quant:
             raise ValueError(f"resnorm: N={N} is not a multiple of quant={quant}")
         if q is None:
-            q = torch.empty((rows, N), dtype=torch.uint8, device=y.device)
+            q = _empty(stream, (rows, N), dtype=torch.uint8, device=y.device)
         if q_scale is None:
-            q_scale = torch.empty((rows, N // quant), dtype=torch.float32 if quant == 128 else torch.uint8,
-                                  device=y.device)
+            q_scale = _empty(stream, (rows, N // quant), dtype=torch.float32 if quant == 128 else torch.uint8,
+                             device=y.device)
         _fits(q, n, "q")
         _fits(q_scale, n // quant, "q_scale")
     else:
         if not (q is None and q_scale is None):
             raise ValueError("resnorm: q and q_scale need quant=32 or 128")
         if z is None:
-            z = torch.empty((rows, N), dtype=torch.bfloat16, device=y.device)
+            z = _empty(stream, (rows, N), dtype=torch.bfloat16, device=y.device)
     if z is not None:
         _fits(z, n, "z")
     p, st = _args("resnorm", stream, (y, ty.bf if y_scale is None else ty.u8, "y"), (y_scale, ty.f32, "y_scale"),
