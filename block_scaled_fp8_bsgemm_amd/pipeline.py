@@ -24,8 +24,8 @@ straight into the residual stream and the next projection's fp8 operand.
 """
 import torch
 
-from . import (actq_e4m3, band_reduce, band_rowq_e4m3, bsgemm_fp8, bsgemm_fp8_lora, lora_plan, lora_shrink, resnorm,
-               rowdq_e4m3, rowq_e4m3)
+from . import (actq_e4m3, band_reduce, band_rowq_e4m3, bsgemm_fp8, bsgemm_fp8_lora, lora_expand, lora_plan,
+               lora_shrink, resnorm, rowdq_e4m3, rowq_e4m3)
 
 
 class WoBStep:
@@ -85,7 +85,10 @@ class WoBServeStep:
       2. lora_plan, lora_shrink   H = x A[a]^T for each row's adapter (x and A hold
                           this rank's part of K, so H and the adapters' share of
                           the output are partial sums like the GEMM's)
-      3. bsgemm_fp8_lora  the partial output, adapters included, as row bands
+      3. bsgemm_fp8_lora  the partial output, adapters included, as row bands; with
+                          fused=False bsgemm_fp8 and lora_expand in place, which a
+                          long batch wants whose rows mix many adapters (bsgemm.h
+                          has the measurements), at one more rounding of C to bf16
       4. band_rowq_e4m3   this rank's band and the other ranks' -> wire rows
       5. resnorm          the gathered wire -> norm, gate, residual, norm, and the
                           next projection's operand (q, q_scale)
@@ -98,7 +101,7 @@ class WoBServeStep:
     PHASES = ("quantize", "plan", "shrink", "gemm", "reduce_quantize", "norm")
 
     def __init__(self, x, B, b_scale, partials, wire_q, wire_s, bands, resid, ids, lora_A, lora_B, lora_scale=None,
-                 post_w=None, gate=None, pre_w=None, alpha=1.0, beta=1.0, eps=1e-6, quant=128):
+                 post_w=None, gate=None, pre_w=None, alpha=1.0, beta=1.0, eps=1e-6, quant=128, fused=True):
         """x bf16 [M, K]; B, b_scale: the weight; partials, wire_q, wire_s, bands as
         for WoBStep; resid bf16 or fp32 [M, N]; ids int32 [M]; lora_A [L, R, K] and
         lora_B [L, N, R] bf16; the rest as for resnorm."""
@@ -114,7 +117,7 @@ class WoBServeStep:
         def new(shape, dtype):
             return torch.empty(shape, dtype=dtype, device=dev)
 
-        self.x, self.B, self.b_scale, self.bands = x, B, b_scale, bands
+        self.x, self.B, self.b_scale, self.bands, self.fused = x, B, b_scale, bands, fused
         self.ids, self.lora_A, self.lora_B, self.lora_scale = ids, lora_A, lora_B, lora_scale
         self.resid, self.wire_q, self.wire_s = resid, wire_q, wire_s
         self.partials = list(partials)
@@ -139,8 +142,13 @@ class WoBServeStep:
         lora_shrink(self.x, self.lora_A, self.lora_plan, self.H)
 
     def gemm(self):
-        bsgemm_fp8_lora(self.A, self.a_scale, self.B, self.b_scale, self.H, self.lora_B, self.ids, self.lora_scale,
-                        self.C.view(-1), bands=self.bands)
+        C = self.C.view(-1)
+        if self.fused:
+            bsgemm_fp8_lora(self.A, self.a_scale, self.B, self.b_scale, self.H, self.lora_B, self.ids, self.lora_scale,
+                            C, bands=self.bands)
+        else:
+            bsgemm_fp8(self.A, self.a_scale, self.B, self.b_scale, C, bands=self.bands)
+            lora_expand(self.H, self.lora_B, self.lora_plan, C, C, self.lora_scale, bands=self.bands)
 
     def reduce_quantize(self):
         band_rowq_e4m3([self.own_band] + self.partials, self.own_q, self.own_s)
