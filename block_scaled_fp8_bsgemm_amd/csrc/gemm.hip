@@ -1507,13 +1507,6 @@ __global__ void __launch_bounds__(NTHREADS) bsgemm_pb_tile_kernel(GemmArgs g) { 
 
 __global__ void __launch_bounds__(NTHREADS) mxgemm_tile_kernel(GemmArgs g) { gemm_tile<MODE_MX>(g); }
 
-// ---- few rows, with adapters -------------------------------------------------
-// The 256-row tile leaves a short batch on N / 256 of the CUs, waiting for B.
-// Here a wave takes 16 RG rows x 16 CG columns by itself, straight from global
-// memory to registers, D K blocks ahead, one wave to a workgroup (two or four
-// side by side took 1.3 to 2.5 times as long: they wait on one CU).  Each K block is the same MFMA on the same fragments, folded in the same order, so the
-// sums are those of the other kernels bit for bit.  The 16-column sub-tiles take B's
-// rows in the order of lora_col, two sub-tiles to a 16-byte piece of C.
 // Workgroup -> tile of rows x cols.  Workgroups are dealt to the XCDs in turn, and a
 // column's row tiles follow each other on one XCD, whose L2 serves B to all but the
 // first.  Where the columns divide by the XCDs they are dealt in turn, which reads
@@ -1530,6 +1523,15 @@ __device__ __forceinline__ bool column_tile(const GemmArgs &g, int rows, int col
     n0 = (int64_t)(even ? t / tm * NUM_XCD + xcd : t / tm) * cols;
     return n0 < g.N;
 }
+
+// ---- few rows, with adapters -------------------------------------------------
+// The 256-row tile leaves a short batch on N / 256 of the CUs, waiting for B.
+// Here a wave takes 16 RG rows x 16 CG columns by itself, straight from global
+// memory to registers, D K blocks ahead, one wave to a workgroup (two or four
+// side by side took 1.3 to 2.5 times as long: they wait on one CU).  Each K block is
+// the same MFMA on the same fragments, folded in the same order, so the sums are
+// those of the other kernels bit for bit.  The 16-column sub-tiles take B's rows in
+// the order of lora_col, two sub-tiles to a 16-byte piece of C.
 
 template <int RG, int CG>
 struct ShortBlock {

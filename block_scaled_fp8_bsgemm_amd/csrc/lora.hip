@@ -205,12 +205,10 @@ __device__ __forceinline__ void shrink_steps(v4f (&acc)[RT][CT], const uint16_t 
 // One workgroup: 16 RT rows of one adapter, 16 CT columns of H.  Its W waves
 // take the K axis in turns of 64 and their partial sums are added in wave
 // order through LDS, so a short batch still spreads K over a CU's waves and
-// the result does not depend on timing.  A lane takes 16 consecutive k of a
-// row in each turn, its first eight to one MFMA and the rest to a second: the
-// contraction may take k in any order as long as both operands do, and a
-// row's four lanes so read 128 consecutive bytes.  The adapter's rows are the
-// MFMA's first operand, which leaves a lane four consecutive columns of one
-// row of H.
+// the result does not depend on timing.  A turn is two MFMAs of 32 k: for each a
+// row's four lanes read 64 consecutive bytes, the two loads its 128.  The adapter's
+// rows are the MFMA's first operand, which leaves a lane four consecutive columns of
+// one row of H.
 template <int RT, int CT, int W, int UN>
 __global__ void __launch_bounds__(W * 64) lora_shrink_kernel(ShrinkArgs g) {
     __shared__ v4f part[W][RT * CT][64];
@@ -422,12 +420,15 @@ static int launch_shrink(const ShrinkArgs &g, hipStream_t stream) {
     return bs_enqueue(lora_shrink_kernel<RT, CT, W, UN>, grid, dim3(64 * W), stream, g);
 }
 
-// Long batches take 64 rows and 64 ranks a workgroup, which reads x once and A
-// once per 64 rows; shorter ones spread the ranks over workgroups, since one CU
-// then waits for fewer of A's bytes.  Graph launches at K = 2048, R = 64, 8
-// adapters, us for (64 rows, 64 ranks) / (16, 64) / (16, 32) / (16, 16): M = 16384:
-// 20.4 / 37.6 / 44.6 / 56.3; M = 4096: 18.5 / 12.8 / 14.5 / 19.6; M = 1024: 18.0 /
-// 12.5 / 9.0 / 10.9; M = 256, mixed: 15.4 / 11.7 / 8.5 / 6.8.
+// Long batches take 64 rows and 64 ranks a workgroup, which reads x once per 64 ranks
+// and A once per 64 rows.  Its 128 KiB of partial sums leave a CU one workgroup, so
+// more than 256 tiles with an adapter take a second round: M = 16384, K = 2048, R = 64
+// takes 20 us up to there and 33 with an adapter on each of its rows, strewn over
+// eight (R = 128: 38 and 51; R = 256: 73 and 87).  Shorter batches spread the ranks over
+// workgroups, since one CU then waits for fewer of A's bytes.  Graph launches at
+// K = 2048, R = 64, 8 adapters, us for (64 rows, 64 ranks) / (16, 64) / (16, 32) /
+// (16, 16): M = 16384: 20.4 / 37.6 / 44.6 / 56.3; M = 4096: 18.5 / 12.8 / 14.5 / 19.6;
+// M = 1024: 18.0 / 12.5 / 9.0 / 10.9; M = 256, mixed: 15.4 / 11.7 / 8.5 / 6.8.
 int bs_launch_lora_shrink(const uint16_t *x, const uint16_t *A, const int32_t *plan, float *H, int64_t M, int64_t K,
                           int L, int R, hipStream_t stream) {
     const ShrinkArgs g = {x, A, plan, H, (int)M, L, R, K};

@@ -14,8 +14,9 @@
 //
 // A row stays in its workgroup's registers from load to store, so each byte is
 // moved once: the kernel is bound by HBM.  16384 wire rows of 7168 with a bf16
-// residual to 1x128 codes: 121 us, 5.8 TB/s; 4096 bf16 rows of 5120 with an fp32
-// residual to bf16 and 1x32 codes: 50 us, 5.5 TB/s; one row of 7168: 4.4 us.
+// residual to 1x128 codes: 118 us, 6.0 TB/s, reading and writing its 676 MiB once; 4096
+// bf16 rows of 5120 with an fp32 residual to bf16 and 1x32 codes: 50 us, 5.5 TB/s;
+// one row of 7168: 4.7 us.
 #include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -327,8 +328,8 @@ int bs_launch_resnorm(const ResnormArgs &all, bool resid_f32, int q_block, hipSt
         // a row has as few lanes as hold it in CPT packs each, so that few are idle
         // (N = 7168: 7 waves of 2 packs, or 4 of 4).  Few rows want the shorter chain
         // of 2 packs, many the fewer waves to join: graph launches of wire rows to
-        // codes at N = 7168, 2 packs / 4: 1 row 4.8 / 5.5 us, 64 rows 4.6 / 5.4, 16384
-        // rows 130 / 126; 2512 bf16 rows of 1536 to bf16: 10.1 / 8.9.
+        // codes at N = 7168, us for 2 packs / 4: 1 row 3.8 / 4.8, 64 rows 4.1 / 5.1, 511
+        // rows 6.7 / 6.9, 1024 rows 11.2 / 10.7, 16384 rows 119 / 117.
         const int rc = g.nch <= 128                       ? launch_t<2, true>(g, resid_f32, q_block, stream)
                        : g.nch <= 1024 && all.rows < 512 ? launch_t<2, false>(g, resid_f32, q_block, stream)
                                                           : launch_t<4, false>(g, resid_f32, q_block, stream);

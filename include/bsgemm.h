@@ -378,7 +378,8 @@ bs_status lora_shrink(const uint16_t *x, const uint16_t *A, const int32_t *plan,
  *   out[m, n] = bf16_rne( base[m, n] + scale[a] * sum_r H[m, r] * B[a, n, r] )
  *
  * for a row with adapter a; out[m] = base[m] for one without.  The sum is fp32;
- * scale * H enters the products as two bf16 (17 bits of significand).  base and
+ * scale * H enters the products as two bf16 (17 bits of significand, within bf16's
+ * largest value).  base and
  * out are row-banded as bsgemm_fp8's C (bands, band_stride as there); elements
  * between bands are untouched.  out may be base itself.
  *
