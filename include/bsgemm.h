@@ -379,9 +379,9 @@ bs_status lora_shrink(const uint16_t *x, const uint16_t *A, const int32_t *plan,
  *
  * for a row with adapter a; out[m] = base[m] for one without.  The sum is fp32;
  * scale * H enters the products as two bf16 (17 bits of significand, within bf16's
- * largest value).  base and
- * out are row-banded as bsgemm_fp8's C (bands, band_stride as there); elements
- * between bands are untouched.  out may be base itself.
+ * largest value).  base and out are row-banded as bsgemm_fp8's C (bands,
+ * band_stride as there); elements between bands are untouched.  out may be base
+ * itself.
  *
  *   H      fp32 [M, R] (what rows without an adapter hold does not matter)
  *   B      bf16 [n_adapters, N, R]
