@@ -24,6 +24,12 @@ library has not been built, importing the functions raises immediately.
                   band_stride=0)
   resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.0, beta=1.0,
           eps=1e-6, quant=0, resid_out=None, z=None, q=None, q_scale=None)
+  bsgemm_fp8_act(A, a_scale, B, b_scale, bias=None, act="none", gated=False, resid=None,
+                 alpha=1.0, beta=1.0, C=None, bands=1, band_stride=0)
+  moe_route(logits, topk, score="softmax", bias=None, groups=1, topk_groups=1, group_top=2,
+            renorm=True, scale=1.0, ids=None, weights=None)
+  moe_fp8(x, ids, weights, W13, s13, W2, s2, base=None, act="silu", out=None, ws=None)
+  moe_fp8_workspace(M, topk, E, I)
 
 Tensors: e4m3 codes are uint8 (or torch.float8_e4m3fn, reinterpreted), bf16
 values are torch.bfloat16 (or int16/uint16 bit patterns), scales float32.
@@ -47,6 +53,7 @@ BS_OK, BS_ERR_INVALID, BS_ERR_UNSUPPORTED, BS_ERR_LAUNCH = 0, 1, 2, 3
 EXPORTS = ("bsgemm_fp8", "band_reduce", "rowq_e4m3", "rowdq_e4m3", "blockq_e4m3", "actq_e4m3",
            "mxgemm_fp8", "mxq_e4m3", "bprepack_e4m3", "bsgemm_fp8_pb", "band_rowq_e4m3",
            "lora_plan", "lora_shrink", "lora_expand", "bsgemm_fp8_lora", "resnorm",
+           "bsgemm_fp8_act", "moe_route", "moe_fp8", "moe_fp8_workspace",
            "bs_status_str")
 
 _lib = None
@@ -84,6 +91,10 @@ def load():
     L.lora_expand.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i32, i64, vp]
     L.bsgemm_fp8_lora.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i64, vp]
     L.resnorm.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i64, i64, i32, i32, f32, f32, f32, vp]
+    L.bsgemm_fp8_act.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, f32, f32, i32, i64, vp]
+    L.moe_route.argtypes = [vp, vp, vp, vp, i64, i64, i32, i32, i32, i32, i32, i32, i32, f32, vp]
+    L.moe_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, vp]
+    L.moe_fp8_workspace.argtypes = [i64, i64, i64, i64, ctypes.POINTER(i64)]
     for f in EXPORTS[:-1]:
         getattr(L, f).restype = ctypes.c_int
     L.bs_status_str.argtypes = [ctypes.c_int]
@@ -607,3 +618,125 @@ def resnorm(y, resid, y_scale=None, post_w=None, gate=None, pre_w=None, alpha=1.
         _check(load().resnorm(*p[:5], gate_row, *p[5:], rows, N, int(resid.dtype is torch.float32), quant, alpha, beta,
                               eps, st), "resnorm")
     return resid_out, z, q, q_scale
+
+
+ACTS = ("none", "relu", "silu", "gelu", "gelu_tanh")   # in the order of bs_act
+SCORES = ("softmax", "sigmoid")
+
+
+def _act_code(act, what):
+    if act not in ACTS:
+        raise ValueError(f"{what}: act must be one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS.index(act)
+
+
+def bsgemm_fp8_act(A, a_scale, B, b_scale, bias=None, act="none", gated=False, resid=None, alpha=1.0, beta=1.0, C=None,
+                   bands=1, band_stride=0, stream=None):
+    """C (bf16 bands) = alpha * resid + beta * act(A x B^T + bias), the product as bsgemm_fp8's; gated: B
+    [2N,K] holds the N gate rows, then the N up rows, and C [M,N] takes act(gate) * up.
+
+    bias: bf16, one value for each row of B, or None.  resid: bf16 in bands as C, or None; C=resid
+    updates it in place.  act: none, relu, silu, gelu or gelu_tanh."""
+    ty = _ty()
+    code = _act_code(act, "bsgemm_fp8_act")
+    M, K = _matrix(A, "A")
+    rows = _matrix(B, "B")[0]
+    N = rows // 2 if gated else rows
+    if B.shape[1] != K or K % 128 or N % 128 or (gated and rows % 2):
+        raise ValueError(f"bsgemm_fp8_act: A is [M,{K}], B {tuple(B.shape)}: one K, and K and N multiples of 128")
+    _is(a_scale, (M, K // 128), "a_scale")
+    _is(b_scale, (rows // 128, K // 128), "b_scale")
+    if bias is not None:
+        _is(bias, (rows,), "bias")
+    need = _band_elems(M, N, bands, band_stride)
+    if resid is not None and resid.numel() < need:
+        raise ValueError(f"resid: {resid.numel()} elements, the call reads {need}")
+    if C is None:
+        C = _empty(stream, need, dtype=ty.torch.bfloat16, device=A.device)
+    _fits(C, need, "C")
+    p, st = _args("bsgemm_fp8_act", stream, (A, ty.u8, "A"), (a_scale, ty.f32, "a_scale"), (B, ty.u8, "B"),
+                  (b_scale, ty.f32, "b_scale"), (bias, ty.bf, "bias"), (resid, ty.bf, "resid"), (C, ty.b16, "C"))
+    if M:
+        _check(load().bsgemm_fp8_act(*p, M, N, K, code, int(bool(gated)), alpha, beta, bands, band_stride, st),
+               "bsgemm_fp8_act")
+    return C
+
+
+def moe_route(logits, topk, score="softmax", bias=None, groups=1, topk_groups=1, group_top=2, renorm=True, scale=1.0,
+              ids=None, weights=None, stream=None):
+    """(ids int32 [M,topk], weights fp32 [M,topk]): each row's topk experts by key = score(logits) + bias
+    (fp32 [E]; it takes part in the choice alone), best first, ties to the lower number, and
+    their scores, scaled and (renorm) divided by their sum.  logits: fp32 or bf16 [M,E].  score:
+    softmax or sigmoid.  groups > 1: only the topk_groups groups of experts of the largest
+    sums of their group_top best keys.  Slots that no expert can fill: id -1, weight 0."""
+    ty = _ty()
+    M, E = _matrix(logits, "logits")
+    if score not in SCORES:
+        raise ValueError(f"moe_route: score must be softmax or sigmoid, got {score!r}")
+    if not 1 <= topk <= E:
+        raise ValueError(f"moe_route: topk must be in [1, {E}], got {topk}")
+    if groups < 1 or E % groups or not 1 <= topk_groups <= groups:
+        raise ValueError(f"moe_route: {groups} groups of {E} experts, of which topk_groups={topk_groups}")
+    if group_top not in (1, 2):
+        raise ValueError(f"moe_route: group_top must be 1 or 2, got {group_top}")
+    if bias is not None:
+        _is(bias, (E,), "bias")
+    if ids is None:
+        ids = _empty(stream, (M, topk), ty.torch.int32, logits.device)
+    if weights is None:
+        weights = _empty(stream, (M, topk), ty.torch.float32, logits.device)
+    _fits(ids, M * topk, "ids")
+    _fits(weights, M * topk, "weights")
+    p, st = _args("moe_route", stream, (logits, ty.resid, "logits"), (bias, ty.f32, "bias"), (ids, ty.i32, "ids"),
+                  (weights, ty.f32, "weights"))
+    if M:
+        _check(load().moe_route(*p, M, E, topk, int(logits.dtype is ty.torch.bfloat16), SCORES.index(score), groups,
+                                topk_groups, group_top, int(bool(renorm)), scale, st), "moe_route")
+    return ids, weights
+
+
+def moe_fp8_workspace(M, topk, E, I):
+    """The bytes of moe_fp8's workspace for M tokens of topk experts each, E experts here."""
+    n = ctypes.c_int64()
+    _check(load().moe_fp8_workspace(M, topk, E, I, ctypes.byref(n)), "moe_fp8_workspace")
+    return n.value
+
+
+def moe_fp8(x, ids, weights, W13, s13, W2, s2, base=None, act="silu", out=None, ws=None, stream=None):
+    """out (bf16 [M,D]) = base + sum over each row's experts e = ids[m,k] of weights[m,k] * W2[e] . (act(W1[e]
+    x[m]) * (W3[e] x[m])), for up to 128 rows and M * topk up to 1024.
+
+    x: bf16 [M,D].  ids int32, weights fp32 [M,topk]; an id outside [0,E) is an empty slot.  W13: e4m3
+    [E,2I,D] (W1's rows, then W3's), s13 fp32 [E,2I/128,D/128]; W2: e4m3 [E,D,I], s2 fp32
+    [E,D/128,I/128].  base: bf16 [M,D] or None; out=base adds in place.  ws: uint8, at least
+    moe_fp8_workspace(M, topk, E, I); calls that may run at the same time need one each (None: a new one)."""
+    ty = _ty()
+    code = _act_code(act, "moe_fp8")
+    M, D = _matrix(x, "x")
+    if not (W2.dim() == 3 and W2.shape[1] == D):
+        raise ValueError(f"W2: shape {tuple(W2.shape)}, expected [E, {D}, I]")
+    E, _, I = W2.shape
+    if D % 128 or I % 128:
+        raise ValueError(f"moe_fp8: D={D} and I={I} must be multiples of 128")
+    _is(W13, (E, 2 * I, D), "W13")
+    _is(s13, (E, 2 * I // 128, D // 128), "s13")
+    _is(s2, (E, D // 128, I // 128), "s2")
+    topk = _matrix(ids, "ids")[1]
+    _is(ids, (M, topk), "ids")
+    _is(weights, (M, topk), "weights")
+    if base is not None:
+        _is(base, (M, D), "base")
+    if out is None:
+        out = _empty(stream, (M, D), ty.torch.bfloat16, x.device)
+    _fits(out, M * D, "out")
+    if M:
+        need = moe_fp8_workspace(M, topk, E, I)
+        if ws is None:
+            ws = _empty(stream, need, ty.torch.uint8, x.device)
+        _fits(ws, need, "ws")
+    p, st = _args("moe_fp8", stream, (x, ty.bf, "x"), (ids, ty.i32, "ids"), (weights, ty.f32, "weights"),
+                  (W13, ty.u8, "W13"), (s13, ty.f32, "s13"), (W2, ty.u8, "W2"), (s2, ty.f32, "s2"),
+                  (base, ty.bf, "base"), (out, ty.bf, "out"), (ws, ty.bytes, "ws"))
+    if M:
+        _check(load().moe_fp8(*p, M, topk, E, D, I, code, st), "moe_fp8")
+    return out

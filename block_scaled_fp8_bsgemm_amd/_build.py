@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbsgemm.so")
 
-SOURCES = ["gemm.hip", "stream.hip", "lora.hip", "resnorm.hip", "abi.cpp"]
+SOURCES = ["gemm.hip", "stream.hip", "lora.hip", "resnorm.hip", "moe.hip", "abi.cpp"]
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -1,8 +1,8 @@
 // abi.cpp -- the extern "C" entry points of libbsgemm (declared, with their
 // contracts, in include/bsgemm.h).  Every argument is checked on the host
 // before anything is enqueued; a rejected call launches nothing and writes
-// nothing.  The kernels themselves live in gemm.hip, stream.hip, lora.hip and
-// resnorm.hip.
+// nothing.  The kernels themselves live in gemm.hip, stream.hip, lora.hip,
+// resnorm.hip and moe.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -19,6 +19,11 @@ constexpr int64_t kMaxRows = (int64_t)1 << 30;  // rows of a batch with adapters
 constexpr int64_t kMaxAdapters = 4096;
 constexpr int64_t kMaxRank = 256;
 constexpr int64_t kMaxNorm = 16384;             // a normed row: it stays in one workgroup's registers
+constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxTopk = 64;                // a chosen expert to a lane
+constexpr int64_t kMaxTokens = 128, kMaxPairs = 1024;   // moe_fp8: the lists that its workgroups hold
+constexpr int64_t kMaxWidth = 65536;            // moe_fp8: D and I
+constexpr int32_t kActs = 5;
 
 struct Range {
     uintptr_t lo, hi;  // [lo, hi)
@@ -343,6 +348,108 @@ bs_status resnorm(const void *y, const float *y_scale, const void *resid, const 
     const ResnormArgs g = {y, y_scale, post_w, gate, resid, resid_out, pre_w, z, q, q_scale,
                            rows, gate_row, (int)(N / 8), alpha, beta, eps};
     return bs_launch_resnorm(g, resid_f32 != 0, q_block, as_stream(stream)) == 0 ? BS_OK : BS_ERR_LAUNCH;
+}
+
+bs_status bsgemm_fp8_act(const uint8_t *A, const float *a_scale, const uint8_t *B, const float *b_scale,
+                         const uint16_t *bias, const uint16_t *resid, uint16_t *C, int64_t M, int64_t N, int64_t K,
+                         int32_t act, int32_t gated, float alpha, float beta, int32_t bands, int64_t band_stride,
+                         void *stream) {
+    if (act < 0 || act >= kActs || (gated != 0 && gated != 1)) return BS_ERR_INVALID;
+    if (!std::isfinite(alpha) || !std::isfinite(beta)) return BS_ERR_INVALID;
+    if (N > 0 && N < kMaxDim && M > 0 && M < kMaxDim) {
+        const int64_t rows = gated ? 2 * N : N;   // of B
+        if (rows >= kMaxDim || (M + 255) / 256 * ((rows + 255) / 256) >= ((int64_t)1 << 23)) return BS_ERR_UNSUPPORTED;
+    }
+    if (!aligned(bias, 16) || !aligned(resid, 16)) return BS_ERR_UNSUPPORTED;
+    const auto more = [&](Range rc) {
+        const Range rr = range_of(resid, resid ? (int64_t)(rc.hi - rc.lo) : 0);
+        if (overlap(rc, range_of(bias, bias ? (gated ? 2 : 1) * N * 2 : 0)) || (resid != C && overlap(rc, rr)) ||
+            (gated && (overlap(rc, range_of(B, 2 * N * K)) || overlap(rc, range_of(b_scale, N / 64 * (K / 128) * 4)))))
+            return BS_ERR_INVALID;
+        return BS_OK;
+    };
+    const auto launch = [&](const uint8_t *a, const float *sa, const uint8_t *b, const float *sb, uint16_t *c,
+                            int64_t m, int64_t n, int64_t k, int64_t band_rows, int64_t stride, hipStream_t st) {
+        return bs_launch_gemm_act(a, sa, b, sb, bias, resid, c, m, n, k, act, gated != 0, alpha, beta, band_rows,
+                                  stride, st);
+    };
+    return blockscale_gemm(launch, more, A, a_scale, B, b_scale, C, M, N, K, bands, band_stride, stream);
+}
+
+bs_status moe_route(const void *logits, const float *bias, int32_t *ids, float *weights, int64_t rows, int64_t E,
+                    int32_t topk, int32_t logits_bf16, int32_t score, int32_t groups, int32_t topk_groups,
+                    int32_t group_top, int32_t renorm, float scale, void *stream) {
+    if (((!logits || !ids || !weights) && rows != 0) || rows < 0 || E <= 0 || topk < 1 || groups < 1)
+        return BS_ERR_INVALID;
+    if ((logits_bf16 | score | renorm) & ~1) return BS_ERR_INVALID;
+    if (topk > E || topk_groups < 1 || topk_groups > groups || !std::isfinite(scale)) return BS_ERR_INVALID;
+    if (group_top != 1 && group_top != 2) return BS_ERR_INVALID;
+    if (E > kMaxExperts || topk > kMaxTopk || groups > 64 || E % groups || rows >= ((int64_t)1 << 40) / E)
+        return BS_ERR_UNSUPPORTED;
+    if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+        return BS_ERR_UNSUPPORTED;
+    const Range ri = range_of(ids, rows * topk * 4), rw = range_of(weights, rows * topk * 4);
+    const Range in[] = {range_of(logits, rows * E * (logits_bf16 ? 2 : 4)), range_of(bias, bias ? E * 4 : 0)};
+    for (const Range &r : in)
+        if (overlap(ri, r) || overlap(rw, r)) return BS_ERR_INVALID;
+    if (overlap(ri, rw)) return BS_ERR_INVALID;
+    if (rows == 0) return BS_OK;
+    const int per = (int)(E / groups);
+    // floor(e * mul / 2^20) = e / per for e < 1024: mul exceeds 2^20 / per by less than
+    // one, so e * mul / 2^20 exceeds e / per by less than 2^-10 <= 1 / per
+    const unsigned mul = ((1u << 20) + (unsigned)per - 1) / (unsigned)per;
+    const RouteArgs g = {logits, bias, ids, weights, rows, (int)E, topk, logits_bf16, score == 0, groups, topk_groups,
+                         group_top, renorm, per, mul, scale};
+    return bs_launch_moe_route(g, as_stream(stream)) == 0 ? BS_OK : BS_ERR_LAUNCH;
+}
+
+}  // extern "C"
+
+namespace {
+
+bs_status moe_dims(int64_t M, int64_t topk, int64_t E, int64_t I) {
+    if (M < 0 || topk <= 0 || E <= 0 || I <= 0) return BS_ERR_INVALID;
+    if (M > kMaxTokens || topk > kMaxTopk || M * topk > kMaxPairs || E > kMaxExperts) return BS_ERR_UNSUPPORTED;
+    if (I % 128 || I > kMaxWidth) return BS_ERR_UNSUPPORTED;
+    return BS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+bs_status moe_fp8_workspace(int64_t M, int64_t topk, int64_t E, int64_t I, int64_t *bytes) {
+    if (!bytes) return BS_ERR_INVALID;
+    if (const bs_status st = moe_dims(M, topk, E, I); st != BS_OK) return st;
+    *bytes = bs_moe_workspace(M, topk, E, I);
+    return BS_OK;
+}
+
+bs_status moe_fp8(const uint16_t *x, const int32_t *ids, const float *weights, const uint8_t *W13, const float *s13,
+                  const uint8_t *W2, const float *s2, const uint16_t *base, uint16_t *out, void *ws, int64_t M,
+                  int64_t topk, int64_t E, int64_t D, int64_t I, int32_t act, void *stream) {
+    if (!W13 || !s13 || !W2 || !s2 || D <= 0 || act < 0 || act >= kActs) return BS_ERR_INVALID;
+    if (const bs_status st = moe_dims(M, topk, E, I); st != BS_OK) return st;
+    if (D % 128 || D > kMaxWidth) return BS_ERR_UNSUPPORTED;
+    if (M == 0) return BS_OK;
+    if (!x || !ids || !weights || !out || !ws) return BS_ERR_INVALID;
+    const void *p16[] = {x, W13, W2, base, out, ws};
+    for (const void *p : p16)
+        if (!aligned(p, 16)) return BS_ERR_UNSUPPORTED;
+    const void *p4[] = {ids, weights, s13, s2};
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return BS_ERR_UNSUPPORTED;
+    const int64_t blocks = E * (I / 128) * (D / 128);
+    const Range in[] = {range_of(x, M * D * 2), range_of(ids, M * topk * 4), range_of(weights, M * topk * 4),
+                        range_of(W13, 2 * E * I * D), range_of(s13, 2 * blocks * 4), range_of(W2, E * I * D),
+                        range_of(s2, blocks * 4), range_of(base, base ? M * D * 2 : 0)};
+    const Range ro = range_of(out, M * D * 2), rws = range_of(ws, bs_moe_workspace(M, topk, E, I));
+    if (overlap(ro, rws)) return BS_ERR_INVALID;
+    for (int i = 0; i < 8; i++)
+        if (overlap(rws, in[i]) || (overlap(ro, in[i]) && !(i == 7 && base == out))) return BS_ERR_INVALID;
+    const MoeArgs g = {x, ids, weights, W13, s13, W2, s2, base, out, ws, (int)M, (int)topk, (int)E, act, D, I, 0,
+                       nullptr, 0};
+    return bs_launch_moe(g, as_stream(stream)) == 0 ? BS_OK : BS_ERR_LAUNCH;
 }
 
 }  // extern "C"

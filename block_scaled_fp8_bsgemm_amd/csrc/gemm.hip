@@ -59,6 +59,7 @@
 
 #include <atomic>
 
+#include "act.hpp"
 #include "codec.hpp"
 #include "launch.hpp"
 #include "lora.hpp"
@@ -260,7 +261,7 @@ __device__ __forceinline__ void wait_dma_and_sync() {
 // column block; their products are the combined scales s[i].
 struct RawScales {
     float sa[TM];
-    float sb;
+    float sb, sb1;   // sb1: gated products only
 };
 
 // The a_scale slots hold the tile's 256 rows so that a lane's 8 values
@@ -286,10 +287,8 @@ __device__ __forceinline__ int mx_scale_row(int p) {
 }
 
 template <int ST>
-__device__ __forceinline__ void read_scales(RawScales &r, int wm, int wn, int frow) {
+__device__ __forceinline__ void read_a_scales(RawScales &r, int wm, int frow) {
     const float *sc = stS<ST>();
-    // this wave's 64 columns lie inside one 128-column b_scale block
-    r.sb = sc[BM + (wn >> 1)];   // wave 4's slot: entries BM, BM+1
     typedef float v4s __attribute__((ext_vector_type(4)));
     const v4s *q = (const v4s *)sc + (wm * 16 + frow);
     const v4s lo = q[0], hi = q[32];
@@ -300,22 +299,75 @@ __device__ __forceinline__ void read_scales(RawScales &r, int wm, int wn, int fr
     }
 }
 
+template <int ST>
+__device__ __forceinline__ void read_scales(RawScales &r, int wm, int wn, int frow) {
+    // this wave's 64 columns lie inside one 128-column b_scale block
+    r.sb = stS<ST>()[BM + (wn >> 1)];   // wave 4's slot: entries BM, BM+1
+    read_a_scales<ST>(r, wm, frow);
+}
+
 __device__ __forceinline__ void combine_scales(float (&s)[TM], const RawScales &r) {
 #pragma unroll
     for (int i = 0; i < TM; i++) s[i] = r.sa[i] * r.sb;
 }
 
+// A K block's combined scales: of row group i and column sub-tile j at(i, j).  Sub-tiles
+// share the wave's one column block, except in a gated product (GLU), whose sub-tiles
+// 0 and 1 are gate columns and 2 and 3 up columns, in another block: there the
+// product of the two scales is formed at each use, for want of 8 registers.
+template <bool GLU> struct Scales {
+    float s[TM];
+    __device__ __forceinline__ float at(int i, int) const { return s[i]; }
+    __device__ __forceinline__ void set(const RawScales &r) { combine_scales(s, r); }
+};
+template <> struct Scales<true> {
+    float sa[TM], sb[2];
+    __device__ __forceinline__ float at(int i, int j) const { return sa[i] * sb[j >> 1]; }
+    __device__ __forceinline__ void set(const RawScales &r) {
+#pragma unroll
+        for (int i = 0; i < TM; i++) sa[i] = r.sa[i];
+        sb[0] = r.sb;
+        sb[1] = r.sb1;
+    }
+};
+
+// Row group 7's scales of the previous block, for its last three products.
+template <bool GLU> struct TailScale {
+    float s;
+    __device__ __forceinline__ float at(int) const { return s; }
+    __device__ __forceinline__ void set(const Scales<GLU> &c) { s = c.at(TM - 1, 0); }
+};
+template <> struct TailScale<true> {
+    float s[2];
+    __device__ __forceinline__ float at(int j) const { return s[j >> 1]; }
+    __device__ __forceinline__ void set(const Scales<true> &c) {
+        s[0] = c.at(TM - 1, 0);
+        s[1] = c.at(TM - 1, 2);
+    }
+};
+
+template <int ST, bool GLU>
+__device__ __forceinline__ void read_block_scales(RawScales &r, int wm, int wn, int frow) {
+    if constexpr (GLU) {   // wave 4's slot: entries BM (gate) and BM + 1 (up)
+        r.sb = stS<ST>()[BM];
+        r.sb1 = stS<ST>()[BM + 1];
+        read_a_scales<ST>(r, wm, frow);
+    } else {
+        read_scales<ST>(r, wm, wn, frow);
+    }
+}
+
 // The first fragments of the K block in stage ST, in the order the first
 // MFMAs use them (A row group 0, then B column groups 0..3), then the scales.
-template <int ST>
-__device__ __forceinline__ void read_head(v8i &a, v8i (&bf)[TN], float (&s)[TM], int wm, int wn,
+template <int ST, bool GLU>
+__device__ __forceinline__ void read_head(v8i &a, v8i (&bf)[TN], Scales<GLU> &s, int wm, int wn,
                                           int frow, int fc) {
     a = lds_frag(stA<ST>(), wm * WM + frow, fc);
 #pragma unroll
     for (int j = 0; j < TN; j++) bf[j] = lds_frag(stB<ST>(), wn * WN + j * 16 + frow, fc);
     RawScales r;
-    read_scales<ST>(r, wm, wn, frow);
-    combine_scales(s, r);
+    read_block_scales<ST, GLU>(r, wm, wn, frow);
+    s.set(r);
 }
 
 // ---- mxfp8 --------------------------------------------------------------
@@ -559,9 +611,9 @@ __device__ __forceinline__ void kblock_pb(v4f (&acc)[TM][TN], v4f (&p)[4], float
 // nowhere and those reads fetch unused values.  NEXT = false leaves both out:
 // the other stage is then filled by the caller (the adapters' H, before this
 // block) and waited for at the barrier.
-template <int ST, int SHIFT = 0, bool NEXT = true>
-__device__ __forceinline__ void kblock(v4f (&acc)[TM][TN], v4f (&p)[4], float &s_tail, v8i &a,
-                                       v8i (&bf)[TN], float (&s)[TM], const Loader &L,
+template <int ST, int SHIFT = 0, bool NEXT = true, bool GLU>
+__device__ __forceinline__ void kblock(v4f (&acc)[TM][TN], v4f (&p)[4], TailScale<GLU> &s_tail, v8i &a,
+                                       v8i (&bf)[TN], Scales<GLU> &s, const Loader &L,
                                        const Panels &P, int kload, bool vload, int wm, int wn,
                                        int frow, int fc, const TileOff &d = TileOff{0, 0, 0}) {
     const uint8_t *as = stA<ST>();
@@ -576,7 +628,7 @@ __device__ __forceinline__ void kblock(v4f (&acc)[TM][TN], v4f (&p)[4], float &s
             wait_dma_and_sync();
             if constexpr (NEXT) {
                 a_next = lds_frag(stA<ST ^ 1>(), wm * WM + frow, fc);
-                read_scales<ST ^ 1>(rn, wm, wn, frow);
+                read_block_scales<ST ^ 1, GLU>(rn, wm, wn, frow);
             }
         }
 #pragma unroll
@@ -586,10 +638,10 @@ __device__ __forceinline__ void kblock(v4f (&acc)[TM][TN], v4f (&p)[4], float &s
                 bf[j], af, (v4f){0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
             if (k >= 3) {
                 const int kp = k - 3;
-                fold4(acc[kp / TN][kp % TN], p[kp & 3], s[kp / TN]);
+                fold4(acc[kp / TN][kp % TN], p[kp & 3], s.at(kp / TN, kp % TN));
             } else {
                 // products 29, 30, 31 of the previous block: row group 7
-                fold4(acc[TM - 1][k + 1], p[(k + 1) & 3], s_tail);
+                fold4(acc[TM - 1][k + 1], p[(k + 1) & 3], s_tail.at(k + 1));
             }
             if (NEXT && i == TM - 1) {
                 bf[j] = lds_frag(stB<ST ^ 1>(), wn * WN + j * 16 + frow, fc);
@@ -602,8 +654,8 @@ __device__ __forceinline__ void kblock(v4f (&acc)[TM][TN], v4f (&p)[4], float &s
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    s_tail = s[TM - 1];
-    if constexpr (NEXT) combine_scales(s, rn);
+    s_tail.set(s);
+    if constexpr (NEXT) s.set(rn);
     a = a_next;
 }
 
@@ -613,6 +665,7 @@ constexpr int MODE_BS = 0, MODE_PB = 1, MODE_MX = 2;
 // XCD-aware and grouped: b runs on XCD b % 8, which is given the contiguous
 // run of tiles [x * per_xcd, (x + 1) * per_xcd), ordered in groups of GROUP_M
 // M-tiles.  False for the padding workgroups past the last tile.
+template <int COLS = BN>
 __device__ __forceinline__ bool tile_of(const GemmArgs &g, int b, int64_t &m0, int64_t &n0) {
     const int T = g.tiles_m * g.tiles_n;
     const int per_xcd = (T + NUM_XCD - 1) / NUM_XCD;
@@ -624,18 +677,20 @@ __device__ __forceinline__ bool tile_of(const GemmArgs &g, int b, int64_t &m0, i
     const int gm = min(GROUP_M, g.tiles_m - first_m);
     const int local = t - group * GROUP_M * g.tiles_n;
     m0 = (int64_t)(first_m + local % gm) * BM;
-    n0 = (int64_t)(local / gm) * BN;
+    n0 = (int64_t)(local / gm) * COLS;
     return true;
 }
 
 // The tile-dependent part of the loader in the tile kernels: descriptors of
 // the tile's row panels and scales, zero past the end of the matrices.
-template <int MODE>
+template <int MODE, bool GLU = false>
 __device__ __forceinline__ Panels panels_of(const GemmArgs &g, int64_t m0, int64_t n0, int wave) {
     const int64_t K = g.K;
     Panels P;
     P.rA = make_rsrc(g.A + m0 * K, (g.M - m0) * K);
-    if (MODE == MODE_PB)
+    if (GLU)   // even waves stage gate rows, odd ones up rows
+        P.rB = make_rsrc(g.B + (n0 + (wave & 1) * g.N) * K, (g.N - n0) * K);
+    else if (MODE == MODE_PB)
         P.rB = make_rsrc(g.B + (n0 / 16) * ((int64_t)g.KB * 2048), (g.N - n0) * K);
     else
         P.rB = make_rsrc(g.B + n0 * K, (g.N - n0) * K);
@@ -647,13 +702,15 @@ __device__ __forceinline__ Panels panels_of(const GemmArgs &g, int64_t m0, int64
         const int nb0 = (int)(n0 / 128);
         P.rS = wave < 4 ? make_rsrc((const float *)g.sa + m0 * g.KB, (g.M - m0) * g.KB * 4)
                         : make_rsrc((const float *)g.sb + (int64_t)nb0 * g.KB,
-                                    (int64_t)(g.NB - nb0) * g.KB * 4);
+                                    (int64_t)((GLU ? 2 : 1) * g.NB - nb0) * g.KB * 4);
     }
     return P;
 }
 
-// The lane-dependent part, the same for every tile.
-template <int MODE>
+// The lane-dependent part, the same for every tile.  GLU: the up rows lie N rows
+// behind the gate rows (WHOLE: in the same descriptor), and of the scale blocks wave 4's
+// lane 0 fetches the gate columns' and lane 1 the up columns'.
+template <int MODE, bool GLU = false, bool WHOLE = false>
 __device__ __forceinline__ void init_loader(Loader &L, const GemmArgs &g, int wave, int lane) {
     const int K = (int)g.K;
     L.rZ = make_rsrc(g.A, 0);
@@ -668,14 +725,15 @@ __device__ __forceinline__ void init_loader(Loader &L, const GemmArgs &g, int wa
     const int chunk = (lane & 7) ^ (lane >> 4);
     L.voff = row * K + chunk * 16;
     L.voff1 = L.voff ^ 64;
-    const int rowB = wave * 32 + (lane >> 4) + 16 * ((lane >> 3) & 1);   // = brow_of(LDS row)
+    const int rowB = (GLU ? (wave >> 1) * 32 + (WHOLE ? (wave & 1) * (int)g.N : 0) : wave * 32) + (lane >> 4) +
+                     16 * ((lane >> 3) & 1);   // = brow_of(LDS row)
     L.voffB = rowB * K + chunk * 16;
     L.voffB1 = L.voffB ^ 64;
     L.k4 = 4 * K;
     // blockscale: waves 0..3 fetch a_scale in the slot order of sa_row;
     // mxfp8: each row's 4 scale bytes in the slot order of mx_scale_row
     L.soff = MODE == MODE_MX ? mx_scale_row(wave * 64 + lane) * (K / 32)
-                             : (wave < 4 ? sa_row(wave * 64 + lane) : lane) * g.KB * 4;
+                             : (wave < 4 ? sa_row(wave * 64 + lane) : GLU ? (lane & 1) * g.NB : lane) * g.KB * 4;
     L.sdst = wave * 256;
 }
 
@@ -683,15 +741,16 @@ __device__ __forceinline__ void init_loader(Loader &L, const GemmArgs &g, int wa
 // under 2^31 bytes, which the host checks), and a tile is a byte offset in
 // the lanes' offsets: range-checked like them, so rows past the end still
 // read zeros, and a tile change needs no new descriptor.
-template <int MODE>
+template <int MODE, bool GLU = false>
 __device__ __forceinline__ Panels whole_panels(const GemmArgs &g, int wave) {
     Panels P;
     P.rA = make_rsrc(g.A, g.M * g.K);
-    P.rB = make_rsrc(g.B, g.N * g.K);
+    P.rB = make_rsrc(g.B, (GLU ? 2 : 1) * g.N * g.K);
     if (MODE == MODE_MX)
         P.rS = wave < 4 ? make_rsrc(g.sa, g.M * (g.K / 32)) : make_rsrc(g.sb, g.N * (g.K / 32));
     else
-        P.rS = wave < 4 ? make_rsrc(g.sa, g.M * g.KB * 4) : make_rsrc(g.sb, (int64_t)g.NB * g.KB * 4);
+        P.rS = wave < 4 ? make_rsrc(g.sa, g.M * g.KB * 4)
+                        : make_rsrc(g.sb, (int64_t)(GLU ? 2 : 1) * g.NB * g.KB * 4);
     return P;
 }
 
@@ -848,6 +907,152 @@ __device__ __forceinline__ void store_tile(const v4f (&acc)[TM][TN], const GemmA
         band_store<MODE>(g, o, i * 16, 0, x);
         band_store<MODE>(g, o, i * 16 + 8, dny, y);
     }
+}
+
+// ---- bias, activation and residual -------------------------------------------
+// The epilogue of bsgemm_fp8_act, on the finished fp32 accumulators before the one
+// rounding to bf16:
+//
+//   t = acc + bias,  v = act(t)  or, gated (GLU),  v = act(t_gate) * t_up
+//   C = alpha * resid + beta * v
+//
+// GLU: B has 2 N rows, gate rows first.  A tile's 256 rows of B are then 128 gate and
+// the same 128 up columns, 32 and 32 to a wave: staged so that sub-tiles 0 and 1
+// are gate columns in the order that brow_of gives them, and 2 and 3 the up columns of
+// the same ones, a lane holds both of each of its 8 columns and the product stays in
+// its registers.
+enum { EPI_NONE, EPI_ACT, EPI_GLU };
+
+struct ActArgs {
+    const uint16_t *bias;    // bf16 [N] (GLU: [2 N]) or null
+    const uint16_t *resid;   // bf16 bands as C, or null; may be C
+    float alpha, beta;
+    int act;
+};
+struct ActGemmArgs {
+    GemmArgs g;
+    ActArgs q;
+};
+
+// Eight columns: t in place of their results.  bias, resid: 8 packed bf16 (zeros where
+// there are none).
+__device__ __forceinline__ void add8(float (&t)[8], u32x4 b) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        t[2 * e] += bf16_lo(b[e]);
+        t[2 * e + 1] += bf16_hi(b[e]);
+    }
+}
+__device__ __forceinline__ void join8(float (&v)[8], u32x4 r, const ActArgs &q) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        v[2 * e] = q.beta * v[2 * e];
+        v[2 * e + 1] = q.beta * v[2 * e + 1];
+        if (q.resid) {
+            v[2 * e] += q.alpha * bf16_lo(r[e]);
+            v[2 * e + 1] += q.alpha * bf16_hi(r[e]);
+        }
+    }
+}
+__device__ __forceinline__ u32x4 load_bias8(const ActArgs &q, int64_t n) {
+    return q.bias ? *(const u32x4 *)(q.bias + n) : (u32x4){0u, 0u, 0u, 0u};
+}
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+    return (u32x4){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+// Element of C of row ml = o.ml0 + dml of a tile, column o.n + dn; negative past M.
+__device__ __forceinline__ int64_t band_at(const GemmArgs &g, const BandOut &o, int dml, int dn) {
+    const int ml = o.ml0 + dml;
+    if (ml >= o.rows) return -1;
+    if (o.br >= BM) return (ml < o.mlb ? o.off0 : o.off1) + o.lane_off + (int64_t)dml * g.N + dn;
+    const uint32_t rr = o.r0 + (uint32_t)ml;
+    return (int64_t)(o.d0 + rr / o.br) * g.band_stride + (int64_t)(rr % o.br) * g.N + o.n + dn;
+}
+__device__ __forceinline__ u32x4 load_resid8(const ActArgs &q, int64_t at) {
+    return __builtin_nontemporal_load((const u32x4 *)(q.resid + (at < 0 ? 0 : at)));
+}
+
+// A tile's accumulators in place of their results (GLU: in sub-tiles 0 and 1).  The
+// residual comes in the pieces of the store (tile_pieces), whole 128-byte row segments,
+// four row groups at a time, and goes to its columns' lanes by the same exchange.
+template <bool GLU>
+__device__ __forceinline__ void act_tile(v4f (&acc)[TM][TN], const GemmArgs &g, const ActArgs &q, int64_t m0,
+                                         int64_t n0, int wm, int wn, int lane) {
+    asm volatile("" : "+v"(lane));   // addresses formed here, not hoisted
+    const int frow = lane & 15, fg = lane >> 4;
+    const bool up = (lane >> 3) & 1;
+    const int64_t n = n0 + wn * (GLU ? 32 : 64);
+    if (n >= g.N) return;   // N % 128 == 0: all of the wave's columns
+    const u32x4 b0 = load_bias8(q, n + 8 * fg), b1 = load_bias8(q, n + 8 * fg + (GLU ? g.N : 32));
+    const BandOut o = GLU ? band_out(g, m0, n + 8 * fg, wm * WM + frow)
+                          : band_out(g, m0, n + 8 * fg + (up ? 32 : 0), wm * WM + (lane & 7));
+#pragma unroll
+    for (int h = 0; h < TM; h += 4) {
+        u32x4 r[4][2] = {};
+        if (q.resid) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                r[i][0] = load_resid8(q, band_at(g, o, (h + i) * 16, 0));
+                if (!GLU) r[i][1] = load_resid8(q, band_at(g, o, (h + i) * 16 + 8, up ? -32 : 32));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v4f(&c)[TN] = acc[h + i];
+            float a[8], b[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                a[e] = c[e >> 2][e & 3];
+                b[e] = c[2 + (e >> 2)][e & 3];
+            }
+            add8(a, b0);
+            add8(b, b1);
+            u32x4 ra = {0u, 0u, 0u, 0u}, rb = ra;
+            if (q.resid && !GLU) {
+                ra = up ? r[i][1] : r[i][0];
+                rb = swap_rows8(up ? r[i][0] : r[i][1]);
+            }
+            if constexpr (GLU) {
+                act_all(a, q.act);
+#pragma unroll
+                for (int e = 0; e < 8; e++) a[e] *= b[e];
+                join8(a, r[i][0], q);
+            } else {
+                float v[16];
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    v[e] = a[e];
+                    v[8 + e] = b[e];
+                }
+                act_all(v, q.act);
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    a[e] = v[e];
+                    b[e] = v[8 + e];
+                }
+                join8(a, ra, q);
+                join8(b, rb, q);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                c[e >> 2][e & 3] = a[e];
+                if (!GLU) c[2 + (e >> 2)][e & 3] = b[e];
+            }
+        }
+    }
+}
+
+// The gated tile's store: 64 bytes of 16 rows to an instruction.
+__device__ __forceinline__ void store_gated_tile(const v4f (&acc)[TM][TN], const GemmArgs &g, int64_t m0, int64_t n0,
+                                                 int wave, int lane) {
+    asm volatile("" : "+v"(lane));
+    const BandOut o = band_out(g, m0, n0 + (wave & 3) * 32 + (lane >> 4) * 8, (wave >> 2) * WM + (lane & 15));
+#pragma unroll
+    for (int i = 0; i < TM; i++)
+        band_store<MODE_BS>(g, o, i * 16, 0,
+                            (u32x4){pack_bf16x2(acc[i][0][0], acc[i][0][1]), pack_bf16x2(acc[i][0][2], acc[i][0][3]),
+                                    pack_bf16x2(acc[i][1][0], acc[i][1][1]), pack_bf16x2(acc[i][1][2], acc[i][1][3])});
 }
 
 // ---- adapters --------------------------------------------------------------
@@ -1060,10 +1265,11 @@ __device__ __forceinline__ void lora_add(v4f (&acc)[TM][TN], const GemmArgs &g, 
 // LDS; MODE_PB: blockscale with the prepacked B loaded into registers;
 // MODE_MX: mxfp8 operands (E8M0 scales per 1x32 block, applied by the scaled
 // MFMA).
-template <int MODE, bool LORA = false>
-__device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs &q = {}) {
+template <int MODE, bool LORA = false, int EPI = EPI_NONE>
+__device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs &q = {}, const ActArgs &ep = {}) {
+    constexpr bool GLU = EPI == EPI_GLU;
     int64_t m0, n0;
-    if (!tile_of(g, blockIdx.x, m0, n0)) return;
+    if (!tile_of<GLU ? BN / 2 : BN>(g, blockIdx.x, m0, n0)) return;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform: keep in SGPRs
@@ -1074,8 +1280,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
     if constexpr (LORA) load_ids(g, q, m0, wave, lane);
     bool any = false;   // whether a row of the tile has an adapter
     Loader L;
-    init_loader<MODE>(L, g, wave, lane);
-    L.P = panels_of<MODE>(g, m0, n0, wave);
+    init_loader<MODE, GLU>(L, g, wave, lane);
+    L.P = panels_of<MODE, GLU>(g, m0, n0, wave);
 
     const int frow = lane & 15;
     const int fc = lane >> 4;   // the lane group: K chunks fc and fc + 4
@@ -1142,7 +1348,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
     // loaded and read before the loop; each block then starts the DMA of the
     // next one (see kblock).
     v8i a, bf[TN];
-    float s[TM];
+    Scales<GLU> s;
     if (KB & 1) {
         load_stage<0>(L, 0);
         wait_dma_and_sync();
@@ -1162,7 +1368,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
     v4f p[4];
 #pragma unroll
     for (int q = 0; q < 4; q++) p[q] = (v4f){0.f, 0.f, 0.f, 0.f};
-    float s_tail = 0.f;
+    TailScale<GLU> s_tail = {};
 
     int kb = 0;
     if (KB & 1) {
@@ -1185,14 +1391,16 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
         }
     }
 #pragma unroll
-    for (int j = 1; j < TN; j++) fold4(acc[TM - 1][j], p[(TM * TN - TN + j) & 3], s_tail);
+    for (int j = 1; j < TN; j++) fold4(acc[TM - 1][j], p[(TM * TN - TN + j) & 3], s_tail.at(j));
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the last (empty) DMA is retired
 
     if constexpr (LORA) {
         if (any) lora_add(acc, g, q, m0, n0 + wn * WN, wm, wave, lane);
     }
-    store_tile<MODE>(acc, g, m0, n0, wave, lane);
+    if constexpr (EPI != EPI_NONE) act_tile<GLU>(acc, g, ep, m0, n0, wm, wn, lane);
+    if constexpr (GLU) store_gated_tile(acc, g, m0, n0, wave, lane);
+    else store_tile<MODE>(acc, g, m0, n0, wave, lane);
 }
 
 // A plain tile's epilogue is split in two, so that neither end of a tile
@@ -1249,9 +1457,9 @@ __device__ __forceinline__ void plain_store_rg(const v4f (&acc)[TM][TN], int i, 
 // row groups 4..6, so at the barrier before row group 7 this wave's DMA has
 // landed once at most those 6 stores are outstanding (vector memory
 // operations retire in issue order).
-template <int ST>
-__device__ __forceinline__ void kblock_first(v4f (&acc)[TM][TN], v4f (&p)[4], float &s_tail, v8i &a,
-                                             v8i (&bf)[TN], float (&s)[TM], const Loader &L,
+template <int ST, bool GLU>
+__device__ __forceinline__ void kblock_first(v4f (&acc)[TM][TN], v4f (&p)[4], TailScale<GLU> &s_tail, v8i &a,
+                                             v8i (&bf)[TN], Scales<GLU> &s, const Loader &L,
                                              const Panels &P, int kload, bool vload, int wm, int wn,
                                              int frow, int fc, __amdgpu_buffer_rsrc_t rC,
                                              int64_t N, const PlainOffsets &o) {
@@ -1269,7 +1477,7 @@ __device__ __forceinline__ void kblock_first(v4f (&acc)[TM][TN], v4f (&p)[4], fl
             __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * (7 - TAIL_RG)));
             barrier_lds_only();
             a_next = lds_frag(stA<ST ^ 1>(), wm * WM + frow, fc);
-            read_scales<ST ^ 1>(rn, wm, wn, frow);
+            read_block_scales<ST ^ 1, GLU>(rn, wm, wn, frow);
         }
 #pragma unroll
         for (int j = 0; j < TN; j++) {
@@ -1287,7 +1495,7 @@ __device__ __forceinline__ void kblock_first(v4f (&acc)[TM][TN], v4f (&p)[4], fl
                 const int kp = k - 3;
 #pragma unroll
                 for (int e = 0; e < 4; e++)
-                    acc[kp / TN][kp % TN][e] = __builtin_fmaf(p[kp & 3][e], s[kp / TN], 0.0f);
+                    acc[kp / TN][kp % TN][e] = __builtin_fmaf(p[kp & 3][e], s.at(kp / TN, kp % TN), 0.0f);
             }
             if (i == TM - 1) {
                 bf[j] = lds_frag(stB<ST ^ 1>(), wn * WN + j * 16 + frow, fc);
@@ -1296,8 +1504,8 @@ __device__ __forceinline__ void kblock_first(v4f (&acc)[TM][TN], v4f (&p)[4], fl
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    s_tail = s[TM - 1];
-    combine_scales(s, rn);
+    s_tail.set(s);
+    s.set(rn);
     a = a_next;
 }
 
@@ -1324,7 +1532,7 @@ __device__ __forceinline__ void kblock_first(v4f (&acc)[TM][TN], v4f (&p)[4], fl
 // time (mxfp8).
 constexpr int DMA_SHIFT = 4;
 
-template <int MODE, int WMC>
+template <int MODE, int WMC, bool GLU = false>
 __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
     constexpr int DSH = WMC == 1 ? DMA_SHIFT : 0;
     constexpr bool MX = MODE == MODE_MX;
@@ -1354,7 +1562,7 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
     // block 0 of every tile sits in stage 1 (K / 128 even)
     const int gq = lane >> 4;   // mxfp8: the lane's 32-wide K group
     v8i a, bf[TN];
-    float s[TM];
+    Scales<GLU> s;
     MxScales x;
     load_stage<1>(L, 0);
     wait_dma_and_sync();
@@ -1364,7 +1572,7 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
     v4f p[4];
 #pragma unroll
     for (int q = 0; q < 4; q++) p[q] = (v4f){0.f, 0.f, 0.f, 0.f};
-    float s_tail = 0.f;
+    TailScale<GLU> s_tail = {};
 
     // The kernel's only argument, read in place from the kernarg segment
     // where each tile needs it (scalar loads), rather than held in SGPRs
@@ -1433,7 +1641,7 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
         if constexpr (!MX) {
             // the last three products of the tile (kblock_first carries none)
 #pragma unroll
-            for (int j = 1; j < TN; j++) fold4(acc[TM - 1][j], p[(TM * TN - TN + j) & 3], s_tail);
+            for (int j = 1; j < TN; j++) fold4(acc[TM - 1][j], p[(TM * TN - TN + j) & 3], s_tail.at(j));
         }
 
         if constexpr (MX) {
@@ -1501,6 +1709,11 @@ __global__ void __launch_bounds__(NTHREADS) bsgemm_tile_kernel(GemmArgs g) { gem
 
 __global__ void __launch_bounds__(NTHREADS) bsgemm_lora_tile_kernel(GemmArgs g, LoraGemmArgs q) {
     gemm_tile<MODE_BS, true>(g, q);
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(NTHREADS) bsgemm_act_tile_kernel(ActGemmArgs a) {
+    gemm_tile<MODE_BS, false, EPI>(a.g, {}, a.q);
 }
 
 __global__ void __launch_bounds__(NTHREADS) bsgemm_pb_tile_kernel(GemmArgs g) { gemm_tile<MODE_PB>(g); }
@@ -1732,22 +1945,25 @@ __device__ __forceinline__ void mid_load(const MidLoader &L, int kb) {
                                              kb * 4, 0, 0);
 }
 
-template <int ST>
-__device__ __forceinline__ void mid_block(v4f (&acc)[2][2], const MidLoader &L, int kb, int KB, const float *sb, int lane) {
+template <int ST, bool GLU>
+__device__ __forceinline__ void mid_block(v4f (&acc)[2][2], const MidLoader &L, int kb, int KB, const float *sb,
+                                          const float *sb1, int lane) {
     const int frow = lane & 15, fg = lane >> 4, wm = L.wave >> 2, wn = L.wave & 3;
     __builtin_amdgcn_s_waitcnt(0x0F70 | (MID_DMA * (MID_STAGES - 2)));   // vmcnt: block kb is in
     barrier_lds_only();
     mid_load<(ST + MID_STAGES - 1) % MID_STAGES>(L, min(kb + MID_STAGES - 1, KB - 1));
     const uint8_t *st = stM<ST>();
     const float *sc = (const float *)(st + (MID_BM + MID_BN) * BK + L.wave * 256);
-    const float sbk = sb[kb];
+    const float sbk = sb[kb], sbk1 = GLU ? sb1[kb] : 0.f;
     v8i a[2], b[2];
-    float s[2];
+    float s[2][2];
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         a[i] = lds_frag(st, wm * 32 + i * 16 + frow, fg);
         b[i] = lds_frag(st + MID_BM * BK, wn * 32 + i * 16 + frow, fg);
-        s[i] = sc[wm * 32 + i * 16 + frow] * sbk;
+        const float sa = sc[wm * 32 + i * 16 + frow];
+        s[i][0] = sa * sbk;
+        s[i][1] = GLU ? sa * sbk1 : s[i][0];
     }
     v4f p[2][2];
 #pragma unroll
@@ -1759,7 +1975,46 @@ __device__ __forceinline__ void mid_block(v4f (&acc)[2][2], const MidLoader &L, 
 #pragma unroll
     for (int i = 0; i < 2; i++)
 #pragma unroll
-        for (int j = 0; j < 2; j++) fold4(acc[i][j], p[i][j], s[i]);
+        for (int j = 0; j < 2; j++) fold4(acc[i][j], p[i][j], s[i][j]);
+}
+
+// The sums of one tile of 64 rows and 128 rows of B (GLU: 64 gate and the same 64 up
+// columns, 16 and 16 to a wave in its two sub-tiles).
+template <bool GLU>
+__device__ __forceinline__ void mid_sums(v4f (&acc)[2][2], const GemmArgs &g, int64_t m0, int64_t n0, int rows_in,
+                                         int wave, int lane) {
+    const int K = (int)g.K, KB = g.KB;
+    MidLoader L;
+    L.wave = wave;
+    L.rA = make_rsrc(g.A + m0 * K, (int64_t)rows_in * K);
+    if (GLU) L.rB = make_rsrc(g.B + (n0 + (wave & 1) * g.N) * K, (int64_t)(MID_BN / 2) * K);
+    else L.rB = make_rsrc(g.B + n0 * K, (int64_t)MID_BN * K);
+    L.rS = make_rsrc((const float *)g.sa + m0 * KB, (int64_t)rows_in * KB * 4);
+    const int ra = slot_row(8 * wave + (lane >> 3));
+    L.offA = ra * K + ((lane & 7) ^ (ra & 7)) * 16;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        // LDS row r holds B row lora_col of its sub-tile, within the wave's 32 columns
+        // (GLU: row r % 16 of the wave's 16, from the gate or the up rows)
+        const int r = slot_row(8 * (2 * wave + i) + (lane >> 3));
+        const int row = GLU ? (r >> 5) * 16 + (r & 15) : (r & ~31) + lora_col((r >> 4) & 1, r & 15);
+        L.offB[i] = row * K + ((lane & 7) ^ (r & 7)) * 16;
+    }
+    L.offS = lane * KB * 4;
+    const float *sb = (const float *)g.sb + n0 / 128 * KB;
+    const float *sb1 = GLU ? sb + (int64_t)g.NB * KB : nullptr;
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+    mid_load<0>(L, 0);
+    mid_load<1>(L, min(1, KB - 1));
+    for (int kb = 0; kb < KB; kb += MID_STAGES) {
+        mid_block<0, GLU>(acc, L, kb, KB, sb, sb1, lane);
+        if (kb + 1 < KB) mid_block<1, GLU>(acc, L, kb + 1, KB, sb, sb1, lane);
+        if (kb + 2 < KB) mid_block<2, GLU>(acc, L, kb + 2, KB, sb, sb1, lane);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the DMA past the last block is retired
 }
 
 __global__ void __launch_bounds__(NTHREADS) bsgemm_lora_mid_kernel(GemmArgs g, LoraGemmArgs q) {
@@ -1768,40 +2023,160 @@ __global__ void __launch_bounds__(NTHREADS) bsgemm_lora_mid_kernel(GemmArgs g, L
     int64_t m0, n0;
     if (!column_tile(g, MID_BM, MID_BN, m0, n0)) return;
     const int rows_in = (int)(g.M - m0 < MID_BM ? g.M - m0 : MID_BM);
-    const int K = (int)g.K, KB = g.KB;
-    MidLoader L;
-    L.wave = wave;
-    L.rA = make_rsrc(g.A + m0 * K, (int64_t)rows_in * K);
-    L.rB = make_rsrc(g.B + n0 * K, (int64_t)MID_BN * K);
-    L.rS = make_rsrc((const float *)g.sa + m0 * KB, (int64_t)rows_in * KB * 4);
-    const int ra = slot_row(8 * wave + (lane >> 3));
-    L.offA = ra * K + ((lane & 7) ^ (ra & 7)) * 16;
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        // LDS row r holds B row lora_col of its sub-tile, within the wave's 32 columns
-        const int r = slot_row(8 * (2 * wave + i) + (lane >> 3));
-        L.offB[i] = ((r & ~31) + lora_col((r >> 4) & 1, r & 15)) * K + ((lane & 7) ^ (r & 7)) * 16;
-    }
-    L.offS = lane * KB * 4;
-    const float *sb = (const float *)g.sb + n0 / 128 * KB;
     v4f acc[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-#pragma unroll
-        for (int j = 0; j < 2; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-    mid_load<0>(L, 0);
-    mid_load<1>(L, min(1, KB - 1));
-    for (int kb = 0; kb < KB; kb += MID_STAGES) {
-        mid_block<0>(acc, L, kb, KB, sb, lane);
-        if (kb + 1 < KB) mid_block<1>(acc, L, kb + 1, KB, sb, lane);
-        if (kb + 2 < KB) mid_block<2>(acc, L, kb + 2, KB, sb, lane);
-    }
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the DMA past the last block is retired
+    mid_sums<false>(acc, g, m0, n0, rows_in, wave, lane);
     const int64_t mw = m0 + 32 * (wave >> 2), nw = n0 + 32 * (wave & 3);
     const int rw = rows_in - 32 * (wave >> 2);
     if (rw <= 0) return;
     wave_adapters<2, 2>(acc, g, q, mw, nw, rw < 32 ? rw : 32, lane);
     wave_store<2, 2>(acc, g, mw, nw, rw < 32 ? rw : 32, lane);
+}
+
+// Element of C of row m, column n.
+__device__ __forceinline__ int64_t element_at(const GemmArgs &g, uint32_t m, int64_t n) {
+    const uint32_t br = (uint32_t)g.band_rows, d = m / br;
+    return (int64_t)d * g.band_stride + (int64_t)(m - d * br) * g.N + n;
+}
+
+template <bool GLU>
+__global__ void __launch_bounds__(NTHREADS) bsgemm_act_mid_kernel(ActGemmArgs a) {
+    const GemmArgs &g = a.g;
+    const ActArgs &q = a.q;
+    const int lane = threadIdx.x & 63, frow = lane & 15, fg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int64_t m0, n0;
+    if (!column_tile(g, MID_BM, GLU ? MID_BN / 2 : MID_BN, m0, n0)) return;
+    const int rows_in = (int)(g.M - m0 < MID_BM ? g.M - m0 : MID_BM);
+    v4f acc[2][2];
+    mid_sums<GLU>(acc, g, m0, n0, rows_in, wave, lane);
+    // a lane's columns: 8 of the wave's 32 (GLU: 4 of its 16, gate and up)
+    const int64_t n = n0 + (GLU ? 16 * (wave & 3) + 4 * fg : 32 * (wave & 3) + 8 * fg);
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    u32x4 bias = {0u, 0u, 0u, 0u};
+    if constexpr (GLU) {
+        if (q.bias) {
+            const u32x2 b0 = *(const u32x2 *)(q.bias + n), b1 = *(const u32x2 *)(q.bias + g.N + n);
+            bias = (u32x4){b0[0], b0[1], b1[0], b1[1]};
+        }
+    } else {
+        bias = load_bias8(q, n);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int row = 32 * (wave >> 2) + 16 * i + frow;
+        if (row >= rows_in) continue;
+        const int64_t at = element_at(g, (uint32_t)(m0 + row), n);
+        float t[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) t[e] = acc[i][e >> 2][e & 3];
+        add8(t, bias);
+        if constexpr (GLU) {
+            float v[4] = {t[0], t[1], t[2], t[3]};
+            act_all(v, q.act);
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] *= q.beta * t[4 + e];
+            if (q.resid) {
+                const u32x2 r = *(const u32x2 *)(q.resid + at);
+                v[0] += q.alpha * bf16_lo(r[0]); v[1] += q.alpha * bf16_hi(r[0]);
+                v[2] += q.alpha * bf16_lo(r[1]); v[3] += q.alpha * bf16_hi(r[1]);
+            }
+            *(u32x2 *)(g.C + at) = (u32x2){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        } else {
+            act_all(t, q.act);
+            u32x4 r = {0u, 0u, 0u, 0u};
+            if (q.resid) r = *(const u32x4 *)(q.resid + at);
+            join8(t, r, q);
+            *(u32x4 *)(g.C + at) = pack8(t);
+        }
+    }
+}
+
+// ---- few rows, with bias, activation and residual ------------------------------
+// At most 16 RG rows.  16 rows of B to a workgroup (GLU: 8 gate rows and the up rows
+// of the same columns), whose eight waves take the K blocks in turn: the whole weight
+// is in flight at once, where one wave for all of K waits for a few blocks at a
+// time.  The block products go to LDS, 8 U of them at a time, and are folded in
+// ascending order of K by a lane for each element, so the sums are those of the
+// other kernels bit for bit.
+template <int RG, int U, bool GLU>
+__global__ void __launch_bounds__(NTHREADS) bsgemm_act_rows_kernel(ActGemmArgs a) {
+    constexpr int W = 8, COLS = GLU ? 8 : 16, SB = GLU ? 2 : 1;
+    constexpr int ELEMS = RG * 16 * COLS, PER = (ELEMS + NTHREADS - 1) / NTHREADS;
+    __shared__ v4f prod[W * U][RG][64];
+    __shared__ float scale[W * U][SB][RG * 16];
+    const GemmArgs &g = a.g;
+    const ActArgs &q = a.q;
+    const int tid = threadIdx.x, lane = tid & 63, frow = lane & 15, fg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * COLS, K = g.K;
+    const int KB = g.KB;
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.A, g.M * K), rS = make_rsrc(g.sa, g.M * KB * 4);
+    const uint8_t *B = g.B + (GLU ? n0 + (frow & 7) + (frow >> 3) * g.N : n0 + frow) * K + 16 * fg;
+    const float *sb = (const float *)g.sb + n0 / 128 * KB, *sb1 = sb + (int64_t)g.NB * KB;
+    float acc[PER][SB] = {};
+    for (int k0 = 0; k0 < KB; k0 += W * U) {
+        v8i x[U][RG], b[U];
+        float s[U][RG];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int kb = k0 + u * W + wave;
+            if (kb >= KB) break;
+            const u32x4 lo = __builtin_nontemporal_load((const u32x4 *)(B + (int64_t)kb * 128));
+            const u32x4 hi = __builtin_nontemporal_load((const u32x4 *)(B + (int64_t)kb * 128 + 64));
+            b[u] = (v8i){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+#pragma unroll
+            for (int i = 0; i < RG; i++) {
+                x[u][i] = frag_of(rA, (16 * i + frow) * (int)K + 16 * fg, kb * 128);
+                s[u][i] = __builtin_bit_cast(
+                    float, __builtin_amdgcn_raw_buffer_load_b32(rS, (16 * i + frow) * KB * 4, kb * 4, 0));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int kb = k0 + u * W + wave;
+            if (kb >= KB) break;
+            const float sbk = GLU && fg >= 2 ? sb1[kb] : sb[kb];
+#pragma unroll
+            for (int i = 0; i < RG; i++) {
+                prod[u * W + wave][i][lane] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    b[u], x[u][i], (v4f){0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+                if (fg == 0 || (GLU && fg == 2)) scale[u * W + wave][fg >> 1][16 * i + frow] = s[u][i] * sbk;
+            }
+        }
+        __syncthreads();
+        const int blocks = KB - k0 < W * U ? KB - k0 : W * U;
+#pragma unroll
+        for (int p = 0; p < PER; p++) {
+            const int id = tid + p * NTHREADS;
+            if (id >= ELEMS) break;
+            // element e of lane l's four of row group i: row l % 16, row 4 (l / 16) + e of B's 16
+            const int i = id / (16 * COLS), l = id % (16 * COLS) / 4, e = id & 3;
+#pragma unroll 8
+            for (int k = 0; k < blocks; k++)
+#pragma unroll
+                for (int h = 0; h < SB; h++)
+                    acc[p][h] = __builtin_fmaf(((const float *)&prod[k][i][l + 32 * h])[e], scale[k][h][16 * i + (l & 15)],
+                                               acc[p][h]);
+        }
+        if (k0 + W * U < KB) __syncthreads();   // before the next products
+    }
+#pragma unroll
+    for (int p = 0; p < PER; p++) {
+        const int id = tid + p * NTHREADS;
+        if (id >= ELEMS) break;
+        const int i = id / (16 * COLS), l = id % (16 * COLS) / 4, e = id & 3;
+        const int m = 16 * i + (l & 15);
+        if (m >= g.M) continue;
+        const int64_t n = n0 + 4 * (l >> 4) + e;
+        float v[1] = {acc[p][0]};
+        if (q.bias) v[0] += bf16_lo(q.bias[n]);
+        act_all(v, q.act);
+        if constexpr (GLU) v[0] *= q.bias ? acc[p][1] + bf16_lo(q.bias[g.N + n]) : acc[p][1];
+        v[0] *= q.beta;
+        const int64_t at = element_at(g, (uint32_t)m, n);
+        if (q.resid) v[0] += q.alpha * bf16_lo(q.resid[at]);
+        g.C[at] = (uint16_t)pack_bf16x2(v[0], 0.f);
+    }
 }
 
 // B [N, K] -> the prepacked layout [N/16][K/128][2][64][16 B]: unit u of the
@@ -1908,6 +2283,34 @@ int bs_launch_gemm_lora(const uint8_t *A, const float *sa, const uint8_t *B, con
     if (count(MID_BM, MID_BN) <= 512)
         return bs_enqueue(bsgemm_lora_mid_kernel, grid_of(MID_BM, MID_BN), dim3(NTHREADS), stream, g, q);
     return bs_enqueue(bsgemm_lora_tile_kernel, dim3(gemm_grid(g)), dim3(NTHREADS), stream, g, q);
+}
+
+template <int RG, int U>
+static int launch_act_rows(const ActGemmArgs &a, bool gated, hipStream_t stream) {
+    if (gated)
+        return bs_enqueue(bsgemm_act_rows_kernel<RG, U, true>, dim3((unsigned)(a.g.N / 8)), dim3(NTHREADS), stream, a);
+    return bs_enqueue(bsgemm_act_rows_kernel<RG, U, false>, dim3((unsigned)(a.g.N / 16)), dim3(NTHREADS), stream, a);
+}
+
+int bs_launch_gemm_act(const uint8_t *A, const float *sa, const uint8_t *B, const float *sb, const uint16_t *bias,
+                       const uint16_t *resid, uint16_t *C, int64_t M, int64_t N, int64_t K, int act, bool gated,
+                       float alpha, float beta, int64_t band_rows, int64_t band_stride, hipStream_t stream) {
+    GemmArgs g = gemm_args(A, sa, B, sb, C, M, N, K, band_rows, band_stride);
+    if (gated) g.tiles_n = (int)(N / (BN / 2));
+    const ActGemmArgs a = {g, {bias, resid, alpha, beta, act}};
+    const auto count = [&](int rows, int cols) { return N / cols * ((M + rows - 1) / rows); };
+    const int mid_cols = gated ? MID_BN / 2 : MID_BN;
+    if (M <= 16) return g.KB <= 16 ? launch_act_rows<1, 2>(a, gated, stream) : launch_act_rows<1, 8>(a, gated, stream);
+    if (M <= 32) return launch_act_rows<2, 4>(a, gated, stream);
+    if (M <= 64) return launch_act_rows<4, 2>(a, gated, stream);
+    if (count(MID_BM, mid_cols) <= 512) {
+        const dim3 grid((unsigned)((count(MID_BM, mid_cols) + NUM_XCD - 1) / NUM_XCD * NUM_XCD));
+        return gated ? bs_enqueue(bsgemm_act_mid_kernel<true>, grid, dim3(NTHREADS), stream, a)
+                     : bs_enqueue(bsgemm_act_mid_kernel<false>, grid, dim3(NTHREADS), stream, a);
+    }
+    const dim3 grid(gemm_grid(g));
+    return gated ? bs_enqueue(bsgemm_act_tile_kernel<EPI_GLU>, grid, dim3(NTHREADS), stream, a)
+                 : bs_enqueue(bsgemm_act_tile_kernel<EPI_ACT>, grid, dim3(NTHREADS), stream, a);
 }
 
 int bs_launch_gemm_pb(const uint8_t *A, const float *sa, const uint8_t *Bp, const float *sb,

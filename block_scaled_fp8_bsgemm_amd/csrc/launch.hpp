@@ -50,6 +50,10 @@ int bs_launch_gemm_lora(const uint8_t *A, const float *sa, const uint8_t *B, con
                         const LoraArgs &lora, const int32_t *ids, int64_t M, int64_t N, int64_t K, int64_t band_rows,
                         int64_t band_stride, hipStream_t stream);
 
+int bs_launch_gemm_act(const uint8_t *A, const float *sa, const uint8_t *B, const float *sb, const uint16_t *bias,
+                       const uint16_t *resid, uint16_t *C, int64_t M, int64_t N, int64_t K, int act, bool gated,
+                       float alpha, float beta, int64_t band_rows, int64_t band_stride, hipStream_t stream);
+
 // One row of resnorm, see resnorm.hip.
 struct ResnormArgs {
     const void *y;            // bf16 [rows, N], or e4m3 codes with y_scale
@@ -67,6 +71,40 @@ struct ResnormArgs {
     float alpha, beta, eps;
 };
 int bs_launch_resnorm(const ResnormArgs &g, bool resid_f32, int q_block, hipStream_t stream);
+
+// moe.hip: the experts of a feed-forward block.
+struct RouteArgs {
+    const void *logits;     // fp32 or bf16 [rows, E]
+    const float *bias;      // fp32 [E] or null
+    int32_t *ids;           // int32 [rows, topk]
+    float *weights;         // fp32 [rows, topk]
+    int64_t rows;
+    int E, topk, bf16, softmax, groups, topk_groups, group_top, renorm;
+    int per_group;          // E / groups
+    unsigned group_mul;     // an expert's group is its number * group_mul >> 20
+    float scale;
+};
+int bs_launch_moe_route(RouteArgs g, hipStream_t stream);
+
+struct MoeArgs {
+    const uint16_t *x;      // bf16 [M, D]
+    const int32_t *ids;     // int32 [M, topk]
+    const float *weights;   // fp32 [M, topk]
+    const uint8_t *W13;     // e4m3 [E, 2 I, D]
+    const float *s13;       // fp32 [E, 2 I / 128, D / 128]
+    const uint8_t *W2;      // e4m3 [E, D, I]
+    const float *s2;        // fp32 [E, D / 128, I / 128]
+    const uint16_t *base;   // bf16 [M, D] or null
+    uint16_t *out;          // bf16 [M, D]
+    void *ws;
+    int M, topk, E, act;
+    int64_t D, I;
+    int slots;              // most experts in use
+    uint16_t *h;            // in ws: bf16 [2][M * topk, I], high and low parts
+    int64_t plane;          // elements of one part
+};
+int64_t bs_moe_workspace(int64_t M, int64_t topk, int64_t E, int64_t I);
+int bs_launch_moe(MoeArgs g, hipStream_t stream);
 
 #include <tuple>
 

@@ -33,6 +33,14 @@
  *                next block and its e4m3 operand, in one pass; takes the
  *                gathered fp8 wire or a bf16 output
  *
+ * and the feed-forward block that reads resnorm's operand:
+ *
+ *   bsgemm_fp8_act  bsgemm_fp8 with bias, activation (gated or not) and residual
+ *                in its epilogue
+ *   moe_route    each token's experts and their weights, from the router's logits
+ *   moe_fp8      the experts of a few tokens: both products, the gated activation
+ *                and the weighted sum, in two kernels
+ *
  * Pages defining the operations (cited by title and section):
  *   [PR40757] sglang PR 40757 "[AMD][gfx950] DSV4: fuse wo_b's GEMM with its
  *             all-reduce via mori cco": "What" (block-scale fp8 GEMM followed
@@ -471,6 +479,114 @@ bs_status resnorm(const void *y, const float *y_scale, const void *resid, const 
                   const uint16_t *gate, int64_t gate_row, const uint16_t *pre_w, void *resid_out,
                   uint16_t *z, uint8_t *q, void *q_scale, int64_t rows, int64_t N, int32_t resid_f32,
                   int32_t q_block, float alpha, float beta, float eps, void *stream);
+
+/*
+ * bsgemm_fp8 with bias, activation and residual in its epilogue, the products of a
+ * feed-forward block.  With acc as in bsgemm_fp8:
+ *
+ *   t[m, n] = acc[m, n] + bias[n]
+ *   v[m, n] = act(t[m, n])                  gated = 0: B [N, K]
+ *   v[m, n] = act(t[m, n]) * t[m, N + n]    gated = 1: B [2N, K], the N gate rows first
+ *   C[m, n] = bf16_rne( alpha * resid[m, n] + beta * v[m, n] )
+ *
+ * without the resid term if resid is null, all of it in fp32 and rounded once.  act
+ * (bs_act): none, relu, silu t / (1 + e^-t), gelu t/2 erfc(-t / sqrt 2), gelu_tanh
+ * t / (1 + e^-2u) with u = sqrt(2/pi) (t + 0.044715 t^3); within 2^-15 of their
+ * values, and zero instead of a result below 2^-119.  What is not finite follows these
+ * formulas (silu and both gelus of -infinity are NaN).  acc is bit for bit
+ * bsgemm_fp8's in every batch, so with no bias, activation or residual and beta = 1 so
+ * is C.
+ *
+ *   A, a_scale  as for bsgemm_fp8
+ *   B, b_scale  e4m3 [N or 2N, K], fp32 [N/128 or 2N/128, K/128]
+ *   bias        bf16 [N or 2N] or null
+ *   resid       bf16, in bands as C (bands, band_stride), or null; may be C itself
+ *   C           bf16 bands of M x N
+ *
+ * Requirements: those of bsgemm_fp8, with 2N for N where B's rows count; fewer than
+ * 2^23 tiles of 256 rows of A by 256 of B; alpha and beta finite; bias and resid
+ * 16-byte aligned; C must not overlap an input, except resid == C.
+ */
+typedef enum {
+    BS_ACT_NONE = 0,
+    BS_ACT_RELU = 1,
+    BS_ACT_SILU = 2,
+    BS_ACT_GELU = 3,
+    BS_ACT_GELU_TANH = 4
+} bs_act;
+
+bs_status bsgemm_fp8_act(const uint8_t *A, const float *a_scale, const uint8_t *B, const float *b_scale,
+                         const uint16_t *bias, const uint16_t *resid, uint16_t *C, int64_t M, int64_t N,
+                         int64_t K, int32_t act, int32_t gated, float alpha, float beta, int32_t bands,
+                         int64_t band_stride, void *stream);
+
+/*
+ * Routing: each row's topk experts and their weights, from the router's logits.
+ *
+ *   s[e] = softmax(logits)[e] (score = 0) or 1 / (1 + e^-logits[e]) (score = 1)
+ *   key[e] = s[e] + bias[e]; without bias and with one group, logits[e] itself
+ *   groups > 1: a group is groups-th of the experts, in order; its score is the sum of
+ *     its group_top (1 or 2) largest keys; the topk_groups groups of the largest
+ *     scores are kept, and the others' experts are not chosen
+ *   ids = the topk experts of the largest keys, in descending order
+ *   weights[k] = scale * s[ids[k]], or, with renorm, scale * s[ids[k]] / sum of s[ids]
+ *
+ * The bias so takes part in the choice alone.  Keys, scores and sums are fp64 (which of
+ * two close keys is larger does not go by fp32 roundings); weights are rounded
+ * once.  Equal keys and scores: the lower number first.  An expert whose logit or bias
+ * is -infinity or NaN is not chosen (nor one whose key is NaN); where fewer than
+ * topk can be, the last slots get id -1 and weight 0.  (A NaN or +infinity among a row's
+ * logits makes its softmax weights NaN.)  Where all chosen scores are 0, renorm leaves
+ * 0.
+ *
+ *   logits   fp32 [rows, E], or bf16 if logits_bf16 is 1
+ *   bias     fp32 [E] or null
+ *   ids      int32 [rows, topk];  weights  fp32 [rows, topk]
+ *
+ * Requirements: rows >= 0, rows * E < 2^40; 1 <= E <= 1024; 1 <= topk <= 64, topk <= E;
+ * 1 <= groups <= 64 and groups divides E; 1 <= topk_groups <= groups; scale finite;
+ * logits, bias, ids, weights aligned to their elements; no output overlaps an input or
+ * the other output.
+ */
+bs_status moe_route(const void *logits, const float *bias, int32_t *ids, float *weights, int64_t rows, int64_t E,
+                    int32_t topk, int32_t logits_bf16, int32_t score, int32_t groups, int32_t topk_groups,
+                    int32_t group_top, int32_t renorm, float scale, void *stream);
+
+/*
+ * The experts of a few tokens.  An expert e has W1 and W3 [I, D], stacked in W13[e]
+ * (W1's I rows first), and W2[e] [D, I]:
+ *
+ *   h[m, e] = act(W1[e] x[m]) * (W3[e] x[m])
+ *   out[m] = bf16_rne( base[m] + sum_k weights[m, k] * (W2[e] h[m, e]) ),  e = ids[m, k]
+ *
+ * without base if it is null.  An id outside [0, E) means that the slot is empty (an
+ * expert of another GPU, whose sum is added across GPUs); a row of empty slots is base,
+ * or zero.  An expert named twice by a row counts once, with the sum of the two weights.
+ * Weights are e4m3 values with 128 x 128 fp32 scales; x is not quantized, and h is
+ * carried to 2^-17.  A row's result does not depend on the other rows or their number,
+ * and a value that is not finite, in a row or in an expert that it uses, reaches no
+ * other row.
+ *
+ * Two kernels, bound by reading the weights of the experts in use once.
+ *
+ *   x        bf16 [M, D];  ids  int32 [M, topk];  weights  fp32 [M, topk]
+ *   W13      e4m3 [E, 2I, D];  s13  fp32 [E, 2I/128, D/128]
+ *   W2       e4m3 [E, D, I];   s2   fp32 [E, D/128, I/128]
+ *   base     bf16 [M, D] or null;  out  bf16 [M, D], may be base itself
+ *   ws       workspace of the bytes that moe_fp8_workspace gives, written and read by
+ *            this call alone: calls that may run at the same time need one each
+ *
+ * Requirements: 0 <= M <= 128, 1 <= topk <= 64 and M * topk <= 1024; 1 <= E <= 1024; D and
+ * I positive multiples of 128, at most 65536; x, W13, W2, base, out, ws 16-byte aligned,
+ * the rest 4-byte; out and ws overlap neither each other nor an input, except out ==
+ * base.
+ */
+bs_status moe_fp8(const uint16_t *x, const int32_t *ids, const float *weights, const uint8_t *W13, const float *s13,
+                  const uint8_t *W2, const float *s2, const uint16_t *base, uint16_t *out, void *ws, int64_t M,
+                  int64_t topk, int64_t E, int64_t D, int64_t I, int32_t act, void *stream);
+
+/* The bytes of moe_fp8's workspace, for its limits on M, topk, E and I. */
+bs_status moe_fp8_workspace(int64_t M, int64_t topk, int64_t E, int64_t I, int64_t *bytes);
 
 /* Static, NUL-terminated description of a status code. */
 const char *bs_status_str(bs_status status);
