@@ -74,7 +74,6 @@ constexpr int GROUP_M = 4;
 constexpr int NUM_XCD = 8;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void lds_void;
 
 struct GemmArgs {
     const uint8_t *A;
@@ -236,19 +235,6 @@ __device__ __forceinline__ v8i lds_frag(const uint8_t *st, int r, int g) {
 __device__ __forceinline__ void fold4(v4f &acc, const v4f &p, float s) {
 #pragma unroll
     for (int e = 0; e < 4; e++) acc[e] = __builtin_fmaf(p[e], s, acc[e]);
-}
-
-// A workgroup barrier that leaves vector memory operations in flight:
-// __syncthreads() also fences global memory, which makes the compiler wait
-// for every outstanding store before it.  The caller waits for what the
-// barrier must cover (its DMA) with its own s_waitcnt; the LDS reads issued
-// before are waited for here, and the empty asm statements keep the compiler
-// from moving memory accesses across the barrier.
-__device__ __forceinline__ void barrier_lds_only() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); vmcnt and expcnt not waited for
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
 }
 
 __device__ __forceinline__ void wait_dma_and_sync() {
@@ -2226,7 +2212,7 @@ static int gemm_grid(const GemmArgs &g) {
 // (an atomic per device: concurrent first calls store the same value).
 static std::atomic<int> g_cus[64];
 
-static int stream_cus(hipStream_t stream) {
+int bs_stream_cus(hipStream_t stream) {
     hipDevice_t dev = 0;
     if (hipStreamGetDevice(stream, &dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
     int cus = g_cus[dev].load(std::memory_order_relaxed);
@@ -2243,7 +2229,7 @@ static int stream_cus(hipStream_t stream) {
 // a multiple of 8 so that the XCD of each tile is the one the non-persistent
 // launch gives it.
 static int persistent_grid(const GemmArgs &g, hipStream_t stream) {
-    const int grid = gemm_grid(g), per = stream_cus(stream) / NUM_XCD * NUM_XCD;
+    const int grid = gemm_grid(g), per = bs_stream_cus(stream) / NUM_XCD * NUM_XCD;
     return grid < per ? grid : per;
 }
 

@@ -96,15 +96,13 @@ struct MoeArgs {
     const float *s2;        // fp32 [E, D / 128, I / 128]
     const uint16_t *base;   // bf16 [M, D] or null
     uint16_t *out;          // bf16 [M, D]
-    void *ws;
+    uint16_t *h;            // workspace: bf16 [M * topk, I / 16, 2, 16], high and low parts
     int M, topk, E, act;
     int64_t D, I;
-    int slots;              // most experts in use
-    uint16_t *h;            // in ws: bf16 [2][M * topk, I], high and low parts
-    int64_t plane;          // elements of one part
 };
-int64_t bs_moe_workspace(int64_t M, int64_t topk, int64_t E, int64_t I);
-int bs_launch_moe(MoeArgs g, hipStream_t stream);
+int64_t bs_moe_workspace(int64_t M, int64_t topk, int64_t I);
+int bs_launch_moe(const MoeArgs &g, hipStream_t stream);
+int bs_stream_cus(hipStream_t stream);   // CUs of the stream's device
 
 #include <tuple>
 

@@ -30,6 +30,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, in
                                              0x00020000);
 }
 
+typedef __attribute__((address_space(3))) void lds_void;
+
+// A workgroup barrier that leaves vector memory operations in flight:
+// __syncthreads() also fences global memory, which makes the compiler wait
+// for every outstanding store before it.  The caller waits for what the
+// barrier must cover (its DMA) with its own s_waitcnt; the LDS reads issued
+// before are waited for here, and the empty asm statements keep the compiler
+// from moving memory accesses across the barrier.
+__device__ __forceinline__ void barrier_lds_only() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); vmcnt and expcnt not waited for
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // A byte offset past every descriptor, the largest included.
 constexpr int OUT_OF_RANGE = (int)0x80000000;
 

@@ -150,40 +150,31 @@ __global__ void __launch_bounds__(256) moe_route_kernel(RouteArgs g) {
 // Few tokens are bound by the weights' bytes, 3 D I of each expert in use, so
 // neither product rounds its other operand: x is bf16 as it comes, h is fp32 in two
 // bf16 (hi + lo, 17 bits), and a weight's e4m3 code is a bf16 value exactly.  Products
-// are bf16 MFMAs with fp32 sums, one scale for 64 deep pieces of a 128 x 128 block.
+// are bf16 MFMAs with fp32 sums, one scale for each 64 deep piece of a 128 x 128 block.
 //
-//   moe_up    one workgroup: one expert, 16 columns of W1 and the same of W3; its waves
-//             split D, and their sums are added in wave order
-//   moe_down  one workgroup: 32 columns of out, all experts in ascending order; its
-//             waves split I, each with sums of its own for every token, added in wave
-//             order at the end
+//   moe_up    a workgroup to a CU; an item is one expert, 16 columns of W1 and the same
+//             of W3.  The waves split D, and their sums are added in wave order
+//   moe_down  a workgroup: 16 columns of out; an item is one expert, in ascending
+//             order.  The waves split I; each has its own sums for every token, weighted,
+//             and these are added in wave order at the end
 //
 // How D and I are split does not depend on the tokens, so a token's result is the
-// same in every batch, and nothing is summed by atomics.
+// same in every batch, and no sum depends on timing.
+//
+// The weights come by DMA into two slots of LDS for each wave, 32 rows x 128 bytes (or 16 x
+// 256) to a slot, and the other operand to registers, also for one slot ahead: a wave multiplies
+// one slot while the next is on its way, through the boundaries of items too, and
+// waits for its own loads alone, by their number.  Every load is issued whether or not
+// there is something to load, then out of its descriptor's range, so that the number
+// is always the same.
 
 constexpr int MOE_WAVES = 8, MOE_NT = MOE_WAVES * 64;
-constexpr int MOE_PAIRS = 1024;   // most M * topk
-constexpr int MOE_ROWS = 128;     // most M
-
-// The workspace: the experts in use and their tokens, written by moe_up for moe_down,
-// and h in two planes of bf16 [M * topk, I].
-struct MoeEntry {
-    int at;     // token | pair << 8, pair = token * topk + slot
-    float w;
-};
-struct MoeList {
-    int *count;         // number of experts in use
-    int *expert, *n;    // [slots]: each one's number and how many tokens it has
-    MoeEntry *entry;    // [slots][M]
-};
-__device__ __forceinline__ MoeList moe_list(const MoeArgs &g) {
-    MoeList l;
-    l.count = (int *)g.ws;
-    l.expert = l.count + 64;
-    l.n = l.expert + g.slots;
-    l.entry = (MoeEntry *)(l.n + g.slots);
-    return l;
-}
+constexpr int MOE_PAIRS = 1024;      // most M * topk, and most experts
+constexpr int SLOT = 4096;           // bytes: T tiles of 16 rows of SU 64-byte units
+template <int T> constexpr int SU = 4 / T;
+__shared__ __attribute__((aligned(1024))) uint8_t sW0[MOE_WAVES * SLOT];
+__shared__ __attribute__((aligned(1024))) uint8_t sW1[MOE_WAVES * SLOT];
+template <int ST> __device__ __forceinline__ uint8_t *slot_of(int wave) { return (ST ? sW1 : sW0) + wave * SLOT; }
 
 // Sixteen e4m3 codes as bf16, in order.
 __device__ __forceinline__ void widen16(u32x4 c, v8bf (&v)[2]) {
@@ -198,279 +189,575 @@ __device__ __forceinline__ void widen16(u32x4 c, v8bf (&v)[2]) {
     }
 }
 
+// acc += s p.  The empty statement keeps the sum in its block: moved behind a branch (to the
+// next tile, or past the last unit), it was compiled without the wait states that reading
+// an MFMA's result takes on the branch's other way, and read it too early.
 __device__ __forceinline__ void fold(v4f &acc, const v4f &p, float s) {
 #pragma unroll
     for (int e = 0; e < 4; e++) acc[e] = __builtin_fmaf(p[e], s, acc[e]);
+    asm volatile("" : "+v"(acc));
 }
 
-// The tokens of one workgroup's expert, found from the ids alone.
-struct MoeShared {
-    int ids[MOE_PAIRS];
-    unsigned used[32];          // a bit for each expert
-    int expert, n;
-    MoeEntry entry[MOE_ROWS];
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The experts in use, ascending, and their tokens.
+struct MoeLists {
+    unsigned item[MOE_PAIRS];   // expert | number of its tokens << 10 | first of them in at << 18
+    int at[MOE_PAIRS];          // token | pair << 8, pair = token * topk + slot
+    float w[MOE_PAIRS];         // moe_down: the token's weight
+    int count;
 };
 
-// Finds the `slot`-th expert in use and its tokens (ascending).  False if there are no
-// more.  A token that names an expert in several slots counts once, by the first,
-// with the sum of their weights.
-__device__ __forceinline__ bool moe_find(MoeShared &s, const MoeArgs &g, int slot) {
-    const int tid = threadIdx.x, lane = tid & 63, pairs = g.M * g.topk;
-    if (tid < 32) s.used[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < pairs; i += MOE_NT) {
-        const int e = g.ids[i];
-        const bool ok = (unsigned)e < (unsigned)g.E;
-        s.ids[i] = ok ? e : -1;
-        if (ok) atomicOr(&s.used[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    // every wave: the slot-th set bit of the 32 words
-    unsigned word = lane < 32 ? s.used[lane] : 0;
-    int upto = __popc(word);
+// Every workgroup makes them, from the ids: a counting sort in LDS, in slots that no
+// weights are in yet (scratch).  A token that names an expert in several slots counts once, by
+// the first, with the sum of their weights.  The tokens of an expert stand in the order
+// that its counter gave them, which no result depends on: a token has its own column
+// of an MFMA, and its own sums.
+__device__ __forceinline__ void moe_lists(MoeLists &l, int *scratch, const MoeArgs &g, bool weights) {
+    int *ids = scratch, *hist = ids + MOE_PAIRS, *total = hist + MOE_PAIRS;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, pairs = g.M * g.topk;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up(upto, off, 64);
-        if (lane >= off) upto += v;
-    }
-    const uint64_t hit = __ballot(lane < 32 && upto > slot);
-    const int total = __builtin_amdgcn_readlane(upto, 31);
-    if (slot == 0 && tid == 0 && blockIdx.x == 0) *moe_list(g).count = total;
-    if (!hit) return false;
-    const int l = __ffsll((unsigned long long)hit) - 1;
-    int skip = slot - (__builtin_amdgcn_readlane(upto, l) - __popc(__builtin_amdgcn_readlane((int)word, l)));
-    unsigned w = (unsigned)__builtin_amdgcn_readlane((int)word, l);
-    while (skip-- > 0) w &= w - 1;
-    const int expert = 32 * l + __ffs(w) - 1;
-    if (tid < 64) {   // its tokens
-        int n = 0;
-        for (int m0 = 0; m0 < g.M; m0 += 64) {
-            const int m = m0 + lane;
-            int first = -1;
-            float weight = 0.f;
-            if (m < g.M)
-                for (int k = 0; k < g.topk; k++)
-                    if (s.ids[m * g.topk + k] == expert) {
-                        weight += g.weights[m * g.topk + k];
-                        if (first < 0) first = m * g.topk + k;
-                    }
-            const uint64_t b = __ballot(first >= 0);
-            if (first >= 0) s.entry[n + __popcll(b & ((1ull << lane) - 1))] = MoeEntry{m | first << 8, weight};
-            n += __popcll(b);
-        }
-        if (lane == 0) {
-            s.expert = expert;
-            s.n = n;
+    for (int j = 0; j < 2; j++) {
+        const int i = tid + j * MOE_NT;
+        hist[i] = 0;
+        if (i < pairs) {
+            const int e = g.ids[i];
+            ids[i] = (unsigned)e < (unsigned)g.E ? e : -1;
         }
     }
     __syncthreads();
-    return true;
+    int mine[2];   // the pair's expert, if it is the first of its token to name it
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const int i = tid + j * MOE_NT;
+        mine[j] = i < pairs ? ids[i] : -1;
+        for (int k = i - i % g.topk; k < i && mine[j] >= 0; k++)
+            if (ids[k] == mine[j]) mine[j] = -1;
+        if (mine[j] >= 0) atomicAdd(&hist[mine[j]], 1);
+    }
+    __syncthreads();
+    // experts 2 tid and 2 tid + 1: tokens, and experts in use (<< 16), before them
+    const int n0 = hist[2 * tid], n1 = hist[2 * tid + 1];
+    const int own = n0 + n1 + (((n0 != 0) + (n1 != 0)) << 16);
+    int before = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(before, off, 64);
+        if (lane >= off) before += v;
+    }
+    if (lane == 63) total[wave] = before;
+    __syncthreads();
+    before -= own;
+    for (int w = 0; w < wave; w++) before += total[w];
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const int n = j ? n1 : n0;
+        if (n) {
+            l.item[before >> 16] = (unsigned)(2 * tid + j) | (unsigned)n << 10 | (unsigned)(before & 0xFFFF) << 18;
+            hist[2 * tid + j] = before & 0xFFFF;
+            before += n + (1 << 16);
+        }
+    }
+    if (tid == MOE_NT - 1) l.count = before >> 16;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        if (mine[j] < 0) continue;
+        const int i = tid + j * MOE_NT, m = i / g.topk, pos = atomicAdd(&hist[mine[j]], 1);
+        l.at[pos] = m | i << 8;
+        if (weights) {
+            float w = 0.f;
+            for (int k = i; k < (m + 1) * g.topk; k++)
+                if (ids[k] == mine[j]) w += g.weights[k];
+            l.w[pos] = w;
+        }
+    }
+    __syncthreads();
 }
 
-// A wave's share of `units` pieces of 64.
+// A wave's share of `units` pieces of 64, and the slots that the largest share fills.
 __device__ __forceinline__ int share(int units, int wave) { return units * wave / MOE_WAVES; }
+template <int T> __device__ __forceinline__ int stages_of(int units) {
+    return ((units + MOE_WAVES - 1) / MOE_WAVES + SU<T> - 1) / SU<T>;
+}
 
-// RT x 16 tokens of the workgroup's expert against its 16 + 16 columns.
-template <int RT, int DEPTH>
-__device__ __forceinline__ void moe_up_rows(MoeShared &s, v4f (*part)[2 * RT][64], const MoeArgs &g, int r0, int c0,
-                                            int wave, int lane) {
-    const int fr = lane & 15, fg = lane >> 4;
-    const int64_t D = g.D;
-    const int e = s.expert, n = s.n;
-    const uint8_t *w[2];
-    const float *sc[2];
-    const int DB = (int)(D / 128);
+// T tiles of 16 rows of `pitch` bytes each.
+template <int T> struct Tiles {
+    __amdgpu_buffer_rsrc_t r[T];
+};
+
+// A lane's byte offsets in the SU instructions of a tile, each of whole row segments of
+// 64 SU bytes, 16 bytes a lane.  A row's chunks are permuted by its number so that the 16
+// rows of a fragment read lie in different banks: chunk c of row r is at place c ^ r of
+// the 16 (SU = 4), or c ^ (r / 2) of the 8 (SU = 2, two rows to the banks).
+template <int T> __device__ __forceinline__ int place(int r, int c) { return SU<T> == 4 ? c ^ r : c ^ (r >> 1); }
+template <int T> struct LaneOffsets {
+    int off[SU<T>], chunk[SU<T>];
+};
+template <int T>
+__device__ __forceinline__ LaneOffsets<T> lane_offsets(int pitch, int lane) {
+    LaneOffsets<T> o;
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-        const int64_t col = ((int64_t)e * 2 + h) * g.I + c0;
-        w[h] = g.W13 + (col + fr) * D + 16 * fg;
-        sc[h] = g.s13 + col / 128 * DB;
+    for (int i = 0; i < SU<T>; i++) {
+        const int row = 16 / SU<T> * i + lane / (4 * SU<T>);
+        o.chunk[i] = place<T>(row, lane % (4 * SU<T>));
+        o.off[i] = row * pitch + o.chunk[i] * 16;
     }
-    const uint16_t *x[RT];
+    return o;
+}
+
+// 16 bytes of each lane to consecutive places of LDS.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t *to, int off, int at) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, off, at, 0, 0);
+}
+
+// `units` pieces of 64 bytes from unit u0 on into slot ST.
+template <int ST, int T>
+__device__ __forceinline__ void moe_dma(const Tiles<T> &t, const LaneOffsets<T> &o, int u0, int units, int wave) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the slot's last reads are done
 #pragma unroll
-    for (int i = 0; i < RT; i++) x[i] = g.x + (s.entry[min(r0 + 16 * i + fr, n - 1)].at & 255) * D + 16 * fg;
-    v4f acc[2][RT];
+    for (int h = 0; h < T; h++)
 #pragma unroll
-    for (int h = 0; h < 2; h++)
+        for (int i = 0; i < SU<T>; i++) {
+            const int off = o.chunk[i] < 4 * units ? o.off[i] : OUT_OF_RANGE;
+            dma16(t.r[h], slot_of<ST>(wave) + (h * SU<T> + i) * 1024, off, u0 * 64);
+        }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// All vector memory operations but the last N are done.
+template <int N>
+__device__ __forceinline__ void wait_all_but() {
+    static_assert(N < 64, "vmcnt has 6 bits");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+    asm volatile("" ::: "memory");
+}
+
+// Row fr's 16 codes of unit q, tile h, of slot ST.
+template <int ST, int T>
+__device__ __forceinline__ void slot_frag(v8bf (&w)[2], int h, int q, int wave, int fr, int fg) {
+    widen16(*(const u32x4 *)(slot_of<ST>(wave) + (h * 16 + fr) * 64 * SU<T> + place<T>(fr, 4 * q + fg) * 16), w);
+}
+
+__device__ __forceinline__ v8bf load_v8(__amdgpu_buffer_rsrc_t r, int off, int at) {
+    return __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(r, off, at, 0));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// The other operand's rows come in groups of 16 / Z, each row in Z pieces of 8 values for
+// every 16 of a unit: x in two (its first and second 8), h in four (the two 8s of its
+// high parts, then of its low parts).  The 16 columns of an MFMA are a group's row and
+// piece, column Z r + z: one instruction loads a unit for all of them, however few rows
+// there are, where a piece to an instruction takes Z of them, mostly for rows that are
+// not there, and a CU's rate of loads would bound the kernel.  The weights' first 8 of each 16 go
+// with even pieces and the second 8 with odd ones; the pieces' sums are added at the end.
+__device__ __forceinline__ void group_unit(v4f &acc, const v8bf (&w)[2], const v8bf &x, float scale, bool odd) {
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+    const v4f p0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[0], x, zero, 0, 0, 0);
+    const v4f p1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[1], x, zero, 0, 0, 0);
+    v4f p;
 #pragma unroll
-        for (int i = 0; i < RT; i++) acc[h][i] = (v4f){0.f, 0.f, 0.f, 0.f};
-    const int units = DB * 2, first = share(units, wave), end = share(units, wave + 1);
-    u32x4 wv[DEPTH][2];
-    v8bf xv[DEPTH][RT][2];
-    const auto load = [&](int d, int u) {
-        u = min(u, end - 1);
+    for (int e = 0; e < 4; e++) p[e] = odd ? p1[e] : p0[e];
+    fold(acc, p, scale);
+}
+template <int CTRL> __device__ __forceinline__ float quad_perm(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+// The sum of a row's Z pieces, in each of its lanes.
+template <int Z> __device__ __forceinline__ v4f add_pieces(v4f v) {
 #pragma unroll
-        for (int h = 0; h < 2; h++) wv[d][h] = __builtin_nontemporal_load((const u32x4 *)(w[h] + 64 * (int64_t)u));
+    for (int e = 0; e < 4; e++) {
+        v[e] += quad_perm<0xB1>(v[e]);                // lanes 1, 0, 3, 2
+        if (Z == 4) v[e] += quad_perm<0x4E>(v[e]);    // lanes 2, 3, 0, 1
+    }
+    return v;
+}
+
+// All loads of a stage but the next one's are done: those are `groups` for each unit, the
+// scales and the slot's.
+template <int T, int MAX>
+__device__ __forceinline__ void wait_stage(int groups) {
+    constexpr int N = 1 + SLOT / 1024;
+    if constexpr (MAX == 1) {
+        wait_all_but<SU<T> + N>();
+    } else {
+        if (groups >= MAX) wait_all_but<SU<T> * MAX + N>();
+        else wait_stage<T, MAX - 1>(groups);
+    }
+}
+
+// ----------------------------------------------------------------- moe_up --
+
+// Where a wave is in its work: item `it` (expert, 16 columns from c0 on), the expert's
+// tokens from r0 on (in up to G groups of 8), stage k of the wave's share of D.
+template <int G> struct UpAt {
+    int it, r0, k, expert, first, n, c0, groups;
+    int off[G];   // byte offset of the lane's token's x; out of range past the last one
+};
+struct UpWork {
+    const MoeLists *l;
+    __amdgpu_buffer_rsrc_t x;
+    int items, blocks, stages, first, end;   // blocks: of 16 columns
+    int fr, fg, wave, lane;
+};
+
+template <int G>
+__device__ __forceinline__ void up_tokens(UpAt<G> &a, const UpWork &w, int64_t D) {
+    a.groups = min(max((a.n - a.r0 + 7) >> 3, 1), G);
 #pragma unroll
-        for (int i = 0; i < RT; i++)
+    for (int i = 0; i < G; i++) {
+        const int row = a.r0 + 8 * i + (w.fr >> 1);
+        a.off[i] = row < a.n ? (w.l->at[a.first + row] & 255) * (int)D * 2 + 32 * w.fg + 16 * (w.fr & 1) : OUT_OF_RANGE;
+    }
+}
+template <int G>
+__device__ __forceinline__ void up_item(UpAt<G> &a, const UpWork &w, int64_t D) {
+    if (a.it >= w.items) {
+        a.n = 0;
+    } else {
+        const int t = a.it / w.blocks;
+        a.c0 = (a.it - t * w.blocks) * 16;
+        const unsigned item = (unsigned)uniform((int)w.l->item[t]);
+        a.expert = item & 1023;
+        a.n = item >> 10 & 255;
+        a.first = item >> 18;
+    }
+    up_tokens<G>(a, w, D);
+}
+template <int G>
+__device__ __forceinline__ void up_next(UpAt<G> &a, const UpWork &w, int64_t D) {
+    if (++a.k < w.stages) return;
+    a.k = 0;
+    a.r0 += 8 * G;
+    if (a.r0 < a.n) {
+        up_tokens<G>(a, w, D);
+        return;
+    }
+    a.r0 = 0;
+    a.it += gridDim.x;
+    up_item<G>(a, w, D);
+}
+
+template <int G> struct UpRegs {
+    v8bf x[2][G];
+    float sc;   // lane 8 h + q: the scale of unit q, tile h
+};
+
+// Loads of stage `a` into slot ST and r.
+template <int G, int ST>
+__device__ __forceinline__ void up_load(UpRegs<G> &r, const UpAt<G> &a, const UpWork &w, const MoeArgs &g,
+                                        const LaneOffsets<2> &o) {
+    const int64_t row = (int64_t)a.expert * 2 * g.I + a.c0;
+    const int u0 = w.first + a.k * SU<2>;
+    const int units = a.n > 0 ? min(max(w.end - u0, 0), SU<2>) : 0;
 #pragma unroll
-            for (int q = 0; q < 2; q++) xv[d][i][q] = *(const v8bf *)(x[i] + 64 * (int64_t)u + 8 * q);
-    };
-    if (first < end) {
+    for (int i = 0; i < G; i++) {
+        if (i >= a.groups) break;
 #pragma unroll
-        for (int d = 0; d < DEPTH; d++) load(d, first + d);
-        for (int u0 = first; u0 < end; u0 += DEPTH) {
+        for (int q = 0; q < SU<2>; q++)
+            r.x[q][i] = load_v8(w.x, q < units ? a.off[i] : OUT_OF_RANGE, (u0 + q) * 128);
+    }
+    const int64_t DB = g.D / 128;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(g.s13 + row / 128 * DB, (g.I / 128 * DB + DB) * 4);
+    const int q = w.lane & 7, h = w.lane >> 3;
+    r.sc = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                         rs, h < 2 && q < units ? ((int)(h * g.I / 128 * DB) + (u0 + q) / 2) * 4 : OUT_OF_RANGE, 0, 0));
+    const Tiles<2> t = {make_rsrc(g.W13 + row * g.D, 16 * g.D), make_rsrc(g.W13 + (row + g.I) * g.D, 16 * g.D)};
+    moe_dma<ST, 2>(t, o, u0, units, w.wave);
+}
+
+// The sums of an item's tokens, added over the waves by way of slot ST, which they have
+// just read; act, product, and h as 64 bytes for each 16 columns: their high parts, then
+// their low parts.
+template <int G, int ST>
+__device__ __forceinline__ void up_finish(const v4f (&acc)[2][G], const UpAt<G> &a, const UpWork &w, const MoeArgs &g) {
+    constexpr int GP = 2;   // groups at a time: a slot holds four of a wave's tiles
+    static_assert(G % GP == 0, "whole turns");
 #pragma unroll
-            for (int d = 0; d < DEPTH; d++) {
-                const int u = u0 + d;
-                if (u >= end) break;
+    for (int i0 = 0; i0 < G; i0 += GP) {
+        if (i0 >= a.groups) break;
+        v4f *own = (v4f *)slot_of<ST>(w.wave);
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    v8bf wb[2];
-                    widen16(wv[d][h], wb);
-                    const float scale = sc[h][u >> 1];
+        for (int h = 0; h < 2; h++)
 #pragma unroll
-                    for (int i = 0; i < RT; i++) {
-                        v4f p = {0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < GP; i++) own[(h * GP + i) * 64 + w.lane] = acc[h][i0 + i];
+        barrier_lds_only();
+        const int i = (w.wave - a.it) & (MOE_WAVES - 1);   // another wave from item to item
+        if (i < GP && i0 + i < a.groups) {
+            const int row = a.r0 + 8 * (i0 + i) + (w.fr >> 1);
+            v4f t[2];
 #pragma unroll
-                        for (int q = 0; q < 2; q++)
-                            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[q], xv[d][i][q], p, 0, 0, 0);
-                        fold(acc[h][i], p, scale);
-                    }
+            for (int h = 0; h < 2; h++) {
+                t[h] = (v4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int v = 0; v < MOE_WAVES; v++)
+                    t[h] += ((const v4f *)slot_of<ST>(v))[(h * GP + i) * 64 + w.lane];
+                t[h] = add_pieces<2>(t[h]);
+            }
+            float v[4] = {t[0][0], t[0][1], t[0][2], t[0][3]};
+            act_all(v, g.act);
+            if (row < a.n) {   // even lanes the high parts, odd ones the low parts
+                typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+                v4bf part;
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const float h = v[q] * t[1][q];
+                    const __bf16 hi = (__bf16)h;
+                    part[q] = w.fr & 1 ? (__bf16)(h - (float)hi) : hi;
                 }
-                load(d, u + DEPTH);
-                __builtin_amdgcn_sched_barrier(0);
+                *(v4bf *)(g.h + ((int64_t)(w.l->at[a.first + row] >> 8) * g.I + a.c0) * 2 + 16 * (w.fr & 1) + 4 * w.fg) = part;
             }
         }
+        barrier_lds_only();
     }
+}
+
+// One stage, in slot ST, the next one's loads first.  False after the last.
+template <int G, int ST>
+__device__ __forceinline__ bool up_stage(v4f (&acc)[2][G], UpRegs<G> (&r)[2], UpAt<G> &a, UpAt<G> &next,
+                                         const UpWork &w, const MoeArgs &g, const LaneOffsets<2> &o) {
+    up_load<G, ST ^ 1>(r[ST ^ 1], next, w, g, o);
+    wait_stage<2, G>(next.groups);
+    const int units = min(w.end - (w.first + a.k * SU<2>), SU<2>);
 #pragma unroll
-    for (int h = 0; h < 2; h++)
-#pragma unroll
-        for (int i = 0; i < RT; i++) part[wave][h * RT + i][lane] = acc[h][i];
-    __syncthreads();
-    if (wave < RT) {
-        const int row = r0 + 16 * wave + fr;
-        v4f t[2];
+    for (int q = 0; q < SU<2>; q++) {
+        if (q >= units) break;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            t[h] = (v4f){0.f, 0.f, 0.f, 0.f};
+            v8bf wb[2];
+            slot_frag<ST, 2>(wb, h, q, w.wave, w.fr, w.fg);
+            const float scale = lane_value(r[ST].sc, 8 * h + q);
 #pragma unroll
-            for (int v = 0; v < MOE_WAVES; v++) t[h] += part[v][h * RT + wave][lane];
-        }
-        float a[4] = {t[0][0], t[0][1], t[0][2], t[0][3]};
-        act_all(a, g.act);
-        if (row < n) {
-            typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-            v4bf hi, lo;
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const float h = a[q] * t[1][q];
-                hi[q] = (__bf16)h;
-                lo[q] = (__bf16)(h - (float)hi[q]);
+            for (int i = 0; i < G; i++) {
+                if (i >= a.groups) break;
+                group_unit(acc[h][i], wb, r[ST].x[q][i], scale, w.fr & 1);
             }
-            const int64_t at = (int64_t)(s.entry[row].at >> 8) * g.I + c0 + 4 * fg;
-            *(v4bf *)(g.h + at) = hi;
-            *(v4bf *)(g.h + g.plane + at) = lo;
         }
     }
-    __syncthreads();
+    if (a.k == w.stages - 1) {
+        up_finish<G, ST>(acc, a, w, g);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int i = 0; i < G; i++) acc[h][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+    }
+    a = next;
+    up_next<G>(next, w, g.D);
+    return a.it < w.items;
 }
 
-template <int RTMAX>
+template <int G>
 __global__ void __launch_bounds__(MOE_NT) moe_up_kernel(MoeArgs g) {
-    __shared__ MoeShared s;
-    __shared__ v4f part[MOE_WAVES][2 * RTMAX][64];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int slot = blockIdx.y;
-    if (!moe_find(s, g, slot)) return;
-    const int n = s.n;
-    if (blockIdx.x == 0) {   // the list for moe_down
-        const MoeList l = moe_list(g);
-        if (threadIdx.x == 0) {
-            l.expert[slot] = s.expert;
-            l.n[slot] = n;
-        }
-        if ((int)threadIdx.x < n) l.entry[(int64_t)slot * g.M + threadIdx.x] = s.entry[threadIdx.x];
+    __shared__ MoeLists l;
+    moe_lists(l, (int *)slot_of<0>(0), g, false);
+    UpWork w;
+    w.l = &l;
+    w.lane = threadIdx.x & 63;
+    w.wave = uniform(threadIdx.x >> 6);
+    w.fr = w.lane & 15;
+    w.fg = w.lane >> 4;
+    w.x = make_rsrc(g.x, g.M * g.D * 2);
+    w.blocks = (int)(g.I / 16);
+    w.items = uniform(l.count) * w.blocks;
+    const int units = (int)(g.D / 64);
+    w.stages = stages_of<2>(units);
+    w.first = share(units, w.wave);
+    w.end = share(units, w.wave + 1);
+    const LaneOffsets<2> o = lane_offsets<2>((int)g.D, w.lane);
+    UpAt<G> a = {};
+    a.it = blockIdx.x;
+    if (a.it >= w.items) return;
+    up_item<G>(a, w, g.D);
+    UpAt<G> next = a;
+    UpRegs<G> r[2];
+    v4f acc[2][G];
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int i = 0; i < G; i++) acc[h][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+    up_load<G, 0>(r[0], next, w, g, o);
+    up_next<G>(next, w, g.D);
+    while (up_stage<G, 0>(acc, r, a, next, w, g, o) && up_stage<G, 1>(acc, r, a, next, w, g, o)) {
     }
-    const int c0 = blockIdx.x * 16;
-    for (int r0 = 0; r0 < n; r0 += 16 * RTMAX) {
-        if (RTMAX == 1 || n - r0 <= 16)
-            moe_up_rows<1, 4>(s, (v4f(*)[2][64])part, g, r0, c0, wave, lane);
-        else if (RTMAX == 2 || n - r0 <= 32)
-            moe_up_rows<2, 3>(s, (v4f(*)[4][64])part, g, r0, c0, wave, lane);
-        else
-            moe_up_rows<RTMAX, 2>(s, part, g, r0, c0, wave, lane);
-    }
+    wait_all_but<0>();   // the last (empty) DMA is retired
 }
 
-constexpr int DOWN_CT = 2, DOWN_COLS = 16 * DOWN_CT, DOWN_UNITS = 4;
-constexpr int DOWN_PITCH = DOWN_COLS + 4;   // floats of a token's sums: rows in different banks
+// --------------------------------------------------------------- moe_down --
 
-template <int MMAX>
-__global__ void __launch_bounds__(MOE_NT) moe_down_kernel(MoeArgs g) {
-    __shared__ __attribute__((aligned(16))) float sum[MOE_WAVES][MMAX][DOWN_PITCH];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int fr = lane & 15, fg = lane >> 4;
-    const int64_t I = g.I;
-    const int IB = (int)(I / 128), units = IB * 2;
-    const int first = share(units, wave), end = share(units, wave + 1);
-    const int64_t n0 = (int64_t)blockIdx.x * DOWN_COLS;
-    for (int i = lane; i < MMAX * DOWN_PITCH / 4; i += 64) ((v4f *)sum[wave])[i] = (v4f){0.f, 0.f, 0.f, 0.f};
-    const MoeList l = moe_list(g);
-    const int experts = min(*l.count, g.slots);
-    for (int t = 0; t < experts; t++) {
-        const int e = l.expert[t], n = l.n[t];
-        const MoeEntry *entry = l.entry + (int64_t)t * g.M;
-        const uint8_t *w = g.W2 + ((int64_t)e * g.D + n0 + fr) * I + 16 * fg;
-        const float *sc = g.s2 + ((int64_t)e * (g.D / 128) + n0 / 128) * IB;
-        for (int u0 = first; u0 < end; u0 += DOWN_UNITS) {
-            u32x4 wv[DOWN_UNITS][DOWN_CT];
+// Where a wave is: expert t of the list, its tokens from r0 on (in up to four groups of
+// 4), stage k of the wave's share of I.
+constexpr int DG = 4;
+struct DownAt {
+    int t, r0, k, expert, first, n, groups;
+    int off[DG];   // byte offset of the lane's token's h
+};
+struct DownWork {
+    const MoeLists *l;
+    __amdgpu_buffer_rsrc_t h;
+    int count, stages, first, end;
+    int64_t n0;
+    int fr, fg, wave, lane;
+};
+
+__device__ __forceinline__ void down_tokens(DownAt &a, const DownWork &w, int64_t I) {
+    a.groups = min(max((a.n - a.r0 + 3) >> 2, 1), DG);
 #pragma unroll
-            for (int u = 0; u < DOWN_UNITS; u++)
+    for (int i = 0; i < DG; i++) {
+        const int row = a.r0 + 4 * i + (w.fr >> 2);
+        a.off[i] = row < a.n ? (w.l->at[a.first + row] >> 8) * (int)I * 4 + 64 * w.fg + 16 * (w.fr & 3) : OUT_OF_RANGE;
+    }
+}
+__device__ __forceinline__ void down_item(DownAt &a, const DownWork &w, int64_t I) {
+    if (a.t >= w.count) {
+        a.n = 0;
+    } else {
+        const unsigned item = (unsigned)uniform((int)w.l->item[a.t]);
+        a.expert = item & 1023;
+        a.n = item >> 10 & 255;
+        a.first = item >> 18;
+    }
+    down_tokens(a, w, I);
+}
+__device__ __forceinline__ void down_next(DownAt &a, const DownWork &w, int64_t I) {
+    if (++a.k < w.stages) return;
+    a.k = 0;
+    a.r0 += 4 * DG;
+    if (a.r0 < a.n) {
+        down_tokens(a, w, I);
+        return;
+    }
+    a.r0 = 0;
+    a.t++;
+    down_item(a, w, I);
+}
+
+template <int T> struct DownRegs {
+    v8bf h[SU<T>][DG];
+    float sc;        // lane q: the scale of unit q
+};
+
+// T: tiles of 16 columns to a workgroup.
+template <int T, int ST>
+__device__ __forceinline__ void down_load(DownRegs<T> &r, const DownAt &a, const DownWork &w, const MoeArgs &g,
+                                          const LaneOffsets<T> &o) {
+    const int64_t row = (int64_t)a.expert * g.D + w.n0;
+    const int u0 = w.first + a.k * SU<T>;
+    const int units = a.n > 0 ? min(max(w.end - u0, 0), SU<T>) : 0;
 #pragma unroll
-                for (int j = 0; j < DOWN_CT; j++)
-                    wv[u][j] = __builtin_nontemporal_load((const u32x4 *)(w + j * 16 * I + 64 * (int64_t)min(u0 + u, end - 1)));
-            for (int r0 = 0; r0 < n; r0 += 16) {
-                const MoeEntry x = entry[min(r0 + fr, n - 1)];
-                const uint16_t *h = g.h + (int64_t)(x.at >> 8) * I + 16 * fg;
-                v4f acc[DOWN_CT];
+    for (int i = 0; i < DG; i++) {
+        if (i >= a.groups) break;
 #pragma unroll
-                for (int j = 0; j < DOWN_CT; j++) acc[j] = (v4f){0.f, 0.f, 0.f, 0.f};
+        for (int q = 0; q < SU<T>; q++)
+            r.h[q][i] = load_v8(w.h, q < units ? a.off[i] : OUT_OF_RANGE, (u0 + q) * 256);
+    }
+    const int64_t IB = g.I / 128;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(g.s2 + row / 128 * IB, IB * 4);
+    r.sc = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                         rs, w.lane < units ? (u0 + w.lane) / 2 * 4 : OUT_OF_RANGE, 0, 0));
+    Tiles<T> t;
 #pragma unroll
-                for (int u = 0; u < DOWN_UNITS; u++) {
-                    if (u0 + u >= end) break;
-                    v8bf hv[2][2];
+    for (int j = 0; j < T; j++) t.r[j] = make_rsrc(g.W2 + (row + 16 * j) * g.I, 16 * g.I);
+    moe_dma<ST, T>(t, o, u0, units, w.wave);
+}
+
+// One stage, in slot ST, the next one's loads first.  False after the last.  sum: the
+// wave's own sums, 16 T columns of each token; of a token m, four columns c are at place
+// c ^ (m % 4).
+template <int T, int ST>
+__device__ __forceinline__ bool down_stage(v4f (&acc)[T][DG], DownRegs<T> (&r)[2], DownAt &a, DownAt &next, v4f *sum,
+                                           const DownWork &w, const MoeArgs &g, const LaneOffsets<T> &o) {
+    down_load<T, ST ^ 1>(r[ST ^ 1], next, w, g, o);
+    wait_stage<T, DG>(next.groups);
+    const int units = min(w.end - (w.first + a.k * SU<T>), SU<T>);
 #pragma unroll
-                    for (int p = 0; p < 2; p++)
+    for (int q = 0; q < SU<T>; q++) {
+        if (q >= units) break;
+        const float scale = lane_value(r[ST].sc, q);
 #pragma unroll
-                        for (int q = 0; q < 2; q++)
-                            hv[p][q] = *(const v8bf *)(h + p * g.plane + 64 * (int64_t)(u0 + u) + 8 * q);
-                    const float scale = sc[(u0 + u) >> 1];
+        for (int j = 0; j < T; j++) {
+            v8bf wb[2];
+            slot_frag<ST, T>(wb, j, q, w.wave, w.fr, w.fg);
 #pragma unroll
-                    for (int j = 0; j < DOWN_CT; j++) {
-                        v8bf wb[2];
-                        widen16(wv[u][j], wb);
-                        v4f p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int q = 0; q < 2; q++)
-#pragma unroll
-                            for (int z = 0; z < 2; z++)
-                                p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[q], hv[z][q], p, 0, 0, 0);
-                        fold(acc[j], p, scale);
-                    }
-                }
-                if (r0 + fr < n) {
-                    float *row = &sum[wave][x.at & 255][4 * fg];
-#pragma unroll
-                    for (int j = 0; j < DOWN_CT; j++) {
-                        v4f *d = (v4f *)(row + 16 * j);
-                        v4f v = *d;
-                        fold(v, acc[j], x.w);
-                        *d = v;
-                    }
-                }
+            for (int i = 0; i < DG; i++) {
+                if (i >= a.groups) break;
+                group_unit(acc[j][i], wb, r[ST].h[q][i], scale, w.fr & 1);
             }
         }
     }
+    if (a.k == w.stages - 1) {
+#pragma unroll
+        for (int i = 0; i < DG; i++) {
+            if (i >= a.groups) break;
+            const int row = a.r0 + 4 * i + (w.fr >> 2);
+            const bool mine = (w.fr & 3) == 0 && row < a.n;
+            const int m = mine ? w.l->at[a.first + row] & 255 : 0;
+            const float weight = mine ? w.l->w[a.first + row] : 0.f;
+#pragma unroll
+            for (int j = 0; j < T; j++) {
+                const v4f t = add_pieces<4>(acc[j][i]);
+                if (mine) {
+                    v4f *d = sum + m * 4 * T + 4 * j + (w.fg ^ (m & 3));
+                    v4f s = *d;
+                    fold(s, t, weight);
+                    *d = s;
+                }
+                acc[j][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+            }
+        }
+    }
+    a = next;
+    down_next(next, w, g.I);
+    return a.t < w.count;
+}
+
+template <int T, int MMAX>
+__global__ void __launch_bounds__(MOE_NT) moe_down_kernel(MoeArgs g) {
+    __shared__ MoeLists l;
+    __shared__ v4f sum[MOE_WAVES][MMAX * 4 * T];
+    for (int i = threadIdx.x; i < MOE_WAVES * MMAX * 4 * T; i += MOE_NT) sum[0][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+    moe_lists(l, (int *)slot_of<0>(0), g, true);
+    DownWork w;
+    w.l = &l;
+    w.lane = threadIdx.x & 63;
+    w.wave = uniform(threadIdx.x >> 6);
+    w.fr = w.lane & 15;
+    w.fg = w.lane >> 4;
+    w.h = make_rsrc(g.h, (int64_t)g.M * g.topk * g.I * 4);
+    w.count = uniform(l.count);
+    w.n0 = (int64_t)blockIdx.x * 16 * T;
+    const int units = (int)(g.I / 64);
+    w.stages = stages_of<T>(units);
+    w.first = share(units, w.wave);
+    w.end = share(units, w.wave + 1);
+    const LaneOffsets<T> o = lane_offsets<T>((int)g.I, w.lane);
+    DownAt a = {};
+    if (w.count > 0) {
+        down_item(a, w, g.I);
+        DownAt next = a;
+        DownRegs<T> r[2];
+        v4f acc[T][DG];
+#pragma unroll
+        for (int j = 0; j < T; j++)
+#pragma unroll
+            for (int i = 0; i < DG; i++) acc[j][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+        down_load<T, 0>(r[0], next, w, g, o);
+        down_next(next, w, g.I);
+        while (down_stage<T, 0>(acc, r, a, next, sum[w.wave], w, g, o) &&
+               down_stage<T, 1>(acc, r, a, next, sum[w.wave], w, g, o)) {
+        }
+        wait_all_but<0>();   // the last (empty) DMA is retired
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < g.M * (DOWN_COLS / 4); i += MOE_NT) {
-        const int m = i / (DOWN_COLS / 4), c = i % (DOWN_COLS / 4) * 4;
+    for (int i = threadIdx.x; i < g.M * 4 * T; i += MOE_NT) {
+        const int m = i / (4 * T), c = i % (4 * T);
         v4f v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < MOE_WAVES; q++) v += *(const v4f *)&sum[q][m][c];
-        const int64_t at = m * g.D + n0 + c;
+        for (int k = 0; k < MOE_WAVES; k++) v += sum[k][m * 4 * T + (c ^ (m & 3))];
+        const int64_t at = m * g.D + w.n0 + 4 * c;
         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         if (g.base) {
             const u32x2 b = *(const u32x2 *)(g.base + at);
@@ -502,25 +789,23 @@ int bs_launch_moe_route(RouteArgs g, hipStream_t stream) {
     return 0;
 }
 
-// Bytes of the list, then of the two planes of h.
-static int64_t moe_list_bytes(int64_t M, int64_t slots) {
-    const int64_t n = 256 + slots * 8 + slots * M * (int64_t)sizeof(MoeEntry);
-    return (n + 255) / 256 * 256;
-}
-int64_t bs_moe_workspace(int64_t M, int64_t topk, int64_t E, int64_t I) {
-    const int64_t slots = E < M * topk ? E : M * topk;
-    return moe_list_bytes(M, slots) + 4 * M * topk * I;
+// h: 32 bits for each of its values, of every pair.
+int64_t bs_moe_workspace(int64_t M, int64_t topk, int64_t I) { return 4 * M * topk * I; }
+
+template <int T, int MMAX>
+static int launch_down(const MoeArgs &g, hipStream_t stream) {
+    return bs_enqueue(moe_down_kernel<T, MMAX>, dim3((unsigned)(g.D / (16 * T))), dim3(MOE_NT), stream, g);
 }
 
-int bs_launch_moe(MoeArgs g, hipStream_t stream) {
-    g.slots = g.E < g.M * g.topk ? g.E : g.M * g.topk;
-    g.h = (uint16_t *)((uint8_t *)g.ws + moe_list_bytes(g.M, g.slots));
-    g.plane = (int64_t)g.M * g.topk * g.I;
-    const dim3 up((unsigned)(g.I / 16), (unsigned)g.slots), down((unsigned)(g.D / DOWN_COLS)), block(MOE_NT);
-    int rc = g.M <= 16 ? bs_enqueue(moe_up_kernel<1>, up, block, stream, g)
-                       : bs_enqueue(moe_up_kernel<4>, up, block, stream, g);
+int bs_launch_moe(const MoeArgs &g, hipStream_t stream) {
+    const int64_t slots = g.E < g.M * g.topk ? g.E : g.M * g.topk, items = slots * (g.I / 16);
+    const int64_t wgs = 2 * (int64_t)bs_stream_cus(stream);
+    const dim3 up((unsigned)(items < wgs ? items : wgs)), block(MOE_NT);
+    const int rc = g.M <= 16 ? bs_enqueue(moe_up_kernel<2>, up, block, stream, g)
+                             : bs_enqueue(moe_up_kernel<4>, up, block, stream, g);
     if (rc != 0) return rc;
-    if (g.M <= 16) return bs_enqueue(moe_down_kernel<16>, down, block, stream, g);
-    if (g.M <= 64) return bs_enqueue(moe_down_kernel<64>, down, block, stream, g);
-    return bs_enqueue(moe_down_kernel<128>, down, block, stream, g);
+    // 32 columns to a workgroup while its waves' sums of all tokens fit beside the slots
+    return g.M <= 16   ? launch_down<2, 16>(g, stream)
+           : g.M <= 64 ? launch_down<2, 64>(g, stream)
+                       : launch_down<1, 128>(g, stream);
 }

@@ -563,7 +563,7 @@ bs_status moe_route(const void *logits, const float *bias, int32_t *ids, float *
  * expert of another GPU, whose sum is added across GPUs); a row of empty slots is base,
  * or zero.  An expert named twice by a row counts once, with the sum of the two weights.
  * Weights are e4m3 values with 128 x 128 fp32 scales; x is not quantized, and h is
- * carried to 2^-17.  A row's result does not depend on the other rows or their number,
+ * carried to 2^-17 (within bf16's largest value).  A row's result does not depend on the other rows or their number,
  * and a value that is not finite, in a row or in an expert that it uses, reaches no
  * other row.
  *

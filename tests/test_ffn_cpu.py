@@ -104,8 +104,7 @@ def test_workspace(L):
     n = ctypes.c_int64()
     assert L.moe_fp8_workspace(16, 4, 8, 384, None) == INV and L.moe_fp8_workspace(16, 4, 8, 0, n) == INV
     assert L.moe_fp8_workspace(129, 4, 8, 384, n) == UNS and L.moe_fp8_workspace(16, 4, 8, 100, n) == UNS
-    # the two planes of h, and a list of every expert's tokens
-    assert bs.moe_fp8_workspace(16, 4, 8, 384) >= 4 * 64 * 384 + 8 * 16 * 8
+    assert bs.moe_fp8_workspace(16, 4, 8, 384) >= 4 * 64 * 384   # h in 32 bits
     assert bs.moe_fp8_workspace(1, 1, 1024, 128) < bs.moe_fp8_workspace(128, 8, 1024, 128) < 1 << 24
 
 
