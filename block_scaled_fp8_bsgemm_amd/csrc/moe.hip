@@ -4,6 +4,7 @@
 //   moe_fp8     out[m] = base[m] + sum_e w[m,e] W2[e] (act(W1[e] x[m]) * (W3[e] x[m]))
 //               for a few tokens, the experts' weights e4m3 with fp32 128x128 scales
 #include <hip/hip_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "act.hpp"
@@ -15,18 +16,288 @@ namespace {
 
 // ------------------------------------------------------------------ route --
 
-// A key's order as an unsigned integer: larger key, larger integer; 0 is kept for
-// experts that cannot be chosen.
-__device__ __forceinline__ uint64_t ordered(double v) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);   // -0 ranks as 0
-    return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+// One wave to a row, four rows to a workgroup; expert e is lane e / EPL's, so the lowest
+// lane that has the largest key has the lowest such expert.
+//
+// Keys are fp64 by their definition: a chosen expert's key may lie next to one that is
+// not chosen, and which of two fp32 keys is larger goes by their roundings.  Without bias
+// and groups the key is the logit itself and fp32 is exact.  Otherwise a row is chosen
+// by fp32 keys first, and where two keys (or two groups' sums) that the choice or its
+// order compares lie closer than what fp32 may be off (route_close), it is chosen again by
+// fp64 keys.  That happens to about one row in a hundred of 256 experts with random
+// logits; an fp64 exponential for every expert took as long as all the rest.
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_from(int old, int v) {
+    return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xF, false);
 }
-__device__ __forceinline__ double unordered(uint64_t k) {
-    return __builtin_bit_cast(double, (k >> 63) ? k & 0x7FFFFFFFFFFFFFFFull : ~k);
+// op over the wave's lanes, left in lane 63: from 1, 2, 4, 8 lanes below within each 16, then
+// the 16 below's last lane, then the 32 below's.  `none` stands in where there is no lane.
+template <typename Op>
+__device__ __forceinline__ int wave_reduce(int v, int none, Op op) {
+    v = op(v, dpp_from<0x111, 0xF>(none, v));
+    v = op(v, dpp_from<0x112, 0xF>(none, v));
+    v = op(v, dpp_from<0x114, 0xF>(none, v));
+    v = op(v, dpp_from<0x118, 0xF>(none, v));
+    v = op(v, dpp_from<0x142, 0xA>(none, v));
+    v = op(v, dpp_from<0x143, 0xC>(none, v));
+    return __builtin_amdgcn_readlane(v, 63);
+}
+constexpr int KEY_NONE = INT_MIN;
+__device__ __forceinline__ int wave_max(int v) {
+    return wave_reduce(v, KEY_NONE, [](int a, int b) { return max(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    return __builtin_bit_cast(float, wave_reduce(__builtin_bit_cast(int, v), 0, [](int a, int b) {
+                                  return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+                              }));
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ double max_from(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)dpp_from<CTRL, ROWS>((int)b, (int)b);
+    const uint32_t hi = (uint32_t)dpp_from<CTRL, ROWS>((int)(b >> 32), (int)(b >> 32));
+    const double o = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    return o > v ? o : v;
+}
+__device__ __forceinline__ double wave_max(double v) {
+    v = max_from<0x111, 0xF>(v);
+    v = max_from<0x112, 0xF>(v);
+    v = max_from<0x114, 0xF>(v);
+    v = max_from<0x118, 0xF>(v);
+    v = max_from<0x142, 0xA>(v);
+    v = max_from<0x143, 0xC>(v);
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)b, 63), hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int off) {
-    return (uint64_t)__shfl_xor((unsigned long long)v, off, 64);
+// An fp32 key as an integer of the same order (-0 as 0), and back.
+__device__ __forceinline__ int ordered(float v) {
+    const int b = __builtin_bit_cast(int, v + 0.0f);
+    return b ^ (b >> 31 & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float unordered(int k) { return __builtin_bit_cast(float, k ^ (k >> 31 & 0x7FFFFFFF)); }
+
+__device__ __forceinline__ int first_lane(uint64_t lanes) { return __ffsll((unsigned long long)lanes) - 1; }
+
+// Whether two keys, or sums of two, may be in the other order by fp64.  The hardware's
+// exponential of a is off by (2 a + 2) 2^-24 relative, a < 104.  A sigmoid plus a bias is so
+// off by less than 2^-21 (1 + |key|), since s (1 - s) a < 1/4; a score without bias by less
+// than 2^-16 of itself; and the margins are over four times as much for either two.
+__device__ __forceinline__ bool route_close(float a, float b, bool biased) {
+    const float margin = biased ? 0x1p-17f * (1.0f + fabsf(a) + fabsf(b)) : 0x1p-13f * (a + b);
+    return !(a - b > margin);
+}
+
+// The largest and second largest key of group `lane`, by way of LDS.
+template <typename K>
+__device__ __forceinline__ void group_best(const K *key, const RouteArgs &g, int lane, K none, K &best, K &second) {
+    K a = none, b = none;
+    if (lane < g.groups)
+        for (int i = 0; i < g.per_group; i++) {
+            const K k = key[lane * g.per_group + i];
+            const K low = k < a ? k : a;
+            b = low > b ? low : b;
+            a = k > a ? k : a;
+        }
+    best = a;
+    second = b;
+}
+
+template <int EPL> __device__ __forceinline__ bool group_kept(uint64_t keep, const RouteArgs &g, int lane, int i) {
+    const unsigned group = ((unsigned)(lane * EPL + i) * g.group_mul) >> 20;
+    return keep >> (group & 63) & 1;
+}
+
+// Chooses by fp64 keys: lane k has the k-th expert, or -1.
+template <int EPL>
+__device__ __forceinline__ int choose_f64(const float (&x)[EPL], const RouteArgs &g, double top, double *lds, int lane) {
+    double inv_sum = 1.0;
+    if (g.softmax) {
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) sum += lane * EPL + i < g.E ? exp((double)x[i] - top) : 0.0;
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+        inv_sum = 1.0 / sum;
+    }
+    const double none = -INFINITY;
+    double key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; i++) {
+        const int e = lane * EPL + i;
+        const float b = g.bias && e < g.E ? g.bias[e] : 0.f;
+        double k = g.softmax ? exp((double)x[i] - top) * inv_sum : 1.0 / (1.0 + exp(-(double)x[i]));
+        if (g.bias) k += (double)b;
+        key[i] = e < g.E && x[i] > -INFINITY && b > -INFINITY && k == k ? k : none;
+    }
+    if (g.groups > 1) {
+#pragma unroll
+        for (int i = 0; i < EPL; i++) lds[lane * EPL + i] = key[i];
+        __builtin_amdgcn_wave_barrier();
+        double best, second;
+        group_best(lds, g, lane, none, best, second);
+        if (g.group_top == 2 && second > none) best += second;
+        uint64_t keep = 0;
+        for (int k = 0; k < g.topk_groups; k++) {
+            const double m = wave_max(best);
+            if (m == none) break;
+            const int l = first_lane(__ballot(best == m));
+            keep |= 1ull << l;
+            if (lane == l) best = none;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (!group_kept<EPL>(keep, g, lane, i)) key[i] = none;
+    }
+    int mine = -1;
+    for (int k = 0; k < g.topk; k++) {
+        double m = key[0];
+#pragma unroll
+        for (int i = 1; i < EPL; i++) m = key[i] > m ? key[i] : m;
+        const double best = wave_max(m);
+        if (best == none) break;
+        const int l = first_lane(__ballot(m == best));
+        int at = EPL - 1;
+#pragma unroll
+        for (int i = EPL - 2; i >= 0; i--) at = key[i] == best ? i : at;
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (lane == l && at == i) key[i] = none;
+        const int e = l * EPL + __builtin_amdgcn_readlane(at, l);
+        if (lane == k) mine = e;
+    }
+    return mine;
+}
+
+// Lanes l ^ 1, l ^ 2, l ^ 7 and l ^ 15 (an exchange of pairs, quads and eights whose lanes are
+// alike).
+template <int CTRL> __device__ __forceinline__ void merge_from(int &best, int &second) {
+    const int b = dpp_from<CTRL, 0xF>(KEY_NONE, best), c = dpp_from<CTRL, 0xF>(KEY_NONE, second);
+    second = max(min(best, b), max(second, c));
+    best = max(best, b);
+}
+
+// The sum of a group's largest keys, or its largest, as an ordered key.
+__device__ __forceinline__ int group_score(int best, int second, const RouteArgs &g) {
+    return g.group_top == 2 && second != KEY_NONE ? ordered(unordered(best) + unordered(second)) : best;
+}
+
+// The same by fp32 keys; ok is false where they do not decide it.  Keys are kept as
+// integers, each lane's in descending order with the lower expert first, so that a lane's
+// best is its first.
+template <int EPL>
+__device__ __forceinline__ int choose_f32(const float (&x)[EPL], const RouteArgs &g, float top, int *lds, int lane,
+                                          bool &ok) {
+    constexpr float LOG2E = 1.44269504f;
+    const bool plain = !g.bias && g.groups == 1, biased = g.bias != nullptr;
+    int key[EPL];
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < EPL; i++) key[i] = x[i] > -INFINITY ? ordered(x[i]) : KEY_NONE;   // nor NaN
+    } else {
+        float s[EPL], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) {
+            s[i] = g.softmax ? exp2_fast((x[i] - top) * LOG2E) : rcp_fast(1.0f + exp2_fast(-LOG2E * x[i]));
+            sum += lane * EPL + i < g.E ? s[i] : 0.f;
+        }
+        const float inv = g.softmax && biased ? rcp_fast(wave_sum(sum)) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) {
+            const int e = lane * EPL + i;
+            const float b = biased && e < g.E ? g.bias[e] : 0.f;
+            key[i] = x[i] > -INFINITY && b > -INFINITY ? ordered(s[i] * inv + b) : KEY_NONE;
+        }
+    }
+    ok = plain || !g.softmax || top < INFINITY;
+    if (g.groups > 1) {
+        // the topk_groups best, one by one, and the first one that is left out
+        const int lanes = g.per_group / EPL;   // to a group
+        int best = key[0], second = KEY_NONE, m, last = 0, k = 0;
+        const bool whole = lanes * EPL == g.per_group && (lanes & (lanes - 1)) == 0 && lanes <= 16;
+        if (whole) {   // between the group's lanes, and its score in each of them
+#pragma unroll
+            for (int i = 1; i < EPL; i++) {
+                second = max(second, min(best, key[i]));
+                best = max(best, key[i]);
+            }
+            if (lanes > 1) merge_from<0xB1>(best, second);
+            if (lanes > 2) merge_from<0x4E>(best, second);
+            if (lanes > 4) merge_from<0x141>(best, second);
+            if (lanes > 8) merge_from<0x140>(best, second);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; i++) lds[lane * EPL + i] = key[i];
+            __builtin_amdgcn_wave_barrier();
+            group_best(lds, g, lane, KEY_NONE, best, second);
+        }
+        int score = best == KEY_NONE ? KEY_NONE : group_score(best, second, g);
+        const int own = whole ? lane & -lanes : lane;   // the first lane of the lane's group
+        uint64_t keep = 0;
+        for (; k < g.topk_groups; k++) {
+            m = wave_max(score);
+            if (m == KEY_NONE) break;
+            const int l = first_lane(__ballot(score == m));
+            keep |= 1ull << l;
+            if (own == l) score = KEY_NONE;
+            last = m;
+        }
+        if (k == g.topk_groups) {
+            m = wave_max(score);
+            if (m != KEY_NONE && route_close(unordered(last), unordered(m), biased)) ok = false;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (!(whole ? keep >> own & 1 : group_kept<EPL>(keep, g, lane, i))) key[i] = KEY_NONE;
+    }
+    int id[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; i++) id[i] = i;
+#pragma unroll
+    for (int i = 1; i < EPL; i++)   // insertion: stable
+#pragma unroll
+        for (int j = i; j > 0; j--) {
+            const bool swap = key[j] > key[j - 1];
+            const int a = key[j], b = key[j - 1], c = id[j], d = id[j - 1];
+            key[j] = swap ? b : a;
+            key[j - 1] = swap ? a : b;
+            id[j] = swap ? d : c;
+            id[j - 1] = swap ? c : d;
+        }
+    int mine = -1, chosen = KEY_NONE, m = KEY_NONE;   // lane k's expert and key
+    for (int k = 0; k < g.topk; k++) {
+        m = wave_max(key[0]);
+        if (m == KEY_NONE) break;
+        const int l = first_lane(__ballot(key[0] == m));
+        const int e = l * EPL + __builtin_amdgcn_readlane(id[0], l);
+        if (lane == k) {
+            mine = e;
+            chosen = m;
+        }
+        if (lane == l) {
+#pragma unroll
+            for (int i = 0; i + 1 < EPL; i++) {
+                key[i] = key[i + 1];
+                id[i] = id[i + 1];
+            }
+            key[EPL - 1] = KEY_NONE;
+        }
+    }
+    if (!plain && m != KEY_NONE) {
+        m = wave_max(key[0]);   // the first one that is left out
+        int after = __shfl(chosen, lane + 1 < 64 ? lane + 1 : lane, 64);
+        if (lane == g.topk - 1) after = m;
+        const bool close = chosen != KEY_NONE && after != KEY_NONE && lane < g.topk &&
+                           route_close(unordered(chosen), unordered(after), biased);
+        if (__ballot(close)) ok = false;
+    } else if (!plain) {   // fewer than topk: all of them, in order
+        const int after = __shfl(chosen, lane + 1 < 64 ? lane + 1 : lane, 64);
+        if (__ballot(chosen != KEY_NONE && after != KEY_NONE && lane < 63 &&
+                     route_close(unordered(chosen), unordered(after), biased)))
+            ok = false;
+    }
+    return mine;
 }
 
 __device__ __forceinline__ float load_logit(const RouteArgs &g, int64_t row, int e) {
@@ -34,114 +305,88 @@ __device__ __forceinline__ float load_logit(const RouteArgs &g, int64_t row, int
     return g.bf16 ? bf16_lo(((const uint16_t *)g.logits)[i]) : ((const float *)g.logits)[i];
 }
 
-// One wave to a row, four rows to a workgroup, experts lane, lane + 64, ... to a lane
-// (EPL of them).  Keys are fp64: a chosen expert's key may lie next to one that is
-// not chosen, and which of two fp32 keys is larger would go by their roundings.
-template <int EPL>
+// VEC: fp32 logits whose lanes' EPL are whole and aligned.
+//
+// The weights are fp64 exponentials and quotients, for topk lanes of a wave: with up to 16
+// experts chosen one wave does them for the workgroup's four rows.
+template <int EPL, bool VEC>
 __global__ void __launch_bounds__(256) moe_route_kernel(RouteArgs g) {
-    __shared__ uint64_t skey[4][EPL * 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t row = (int64_t)blockIdx.x * 4 + wave;
-    if (row >= g.rows) return;   // no barrier below: waves share nothing
-    float x[EPL];
-    float top = -INFINITY;
+    __shared__ double lds[4][EPL * 64];
+    __shared__ int chosen[4][64];
+    __shared__ double sums[4];   // softmax: of the row's exponentials, less its largest logit
+    __shared__ float tops[4];    // and that, NaN if a logit is
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row0 = (int64_t)blockIdx.x * 4, row = row0 + wave;
+    if (row < g.rows) {
+        float x[EPL];
+        if constexpr (VEC) {
+            typedef float vec __attribute__((ext_vector_type(EPL == 1 ? 1 : EPL == 2 ? 2 : 4)));
+            constexpr int V = EPL < 4 ? EPL : 4;
+            const bool in = lane * EPL < g.E;
 #pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const int e = lane + 64 * i;
-        x[i] = e < g.E ? load_logit(g, row, e) : -INFINITY;
-        top = fmaxf(top, x[i]);
-    }
-    double inv_sum = 1.0;
-    if (g.softmax) {
+            for (int i = 0; i < EPL; i += V) {
+                vec v;
+                if (in) v = *(const vec *)((const float *)g.logits + row * g.E + lane * EPL + i);
 #pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < EPL; i++) sum += lane + 64 * i < g.E ? exp((double)x[i] - (double)top) : 0.0;
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
-        inv_sum = 1.0 / sum;
-    }
-    const auto score = [&](float v) {
-        return g.softmax ? exp((double)v - (double)top) * inv_sum : 1.0 / (1.0 + exp(-(double)v));
-    };
-    uint64_t key[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        const int e = lane + 64 * i;
-        bool ok = e < g.E && x[i] > -INFINITY;
-        double k = x[i];
-        if (g.bias || g.groups > 1) k = score(x[i]);
-        if (g.bias) {
-            const float b = e < g.E ? g.bias[e] : 0.f;
-            ok = ok && b > -INFINITY;
-            k += (double)b;
-        }
-        key[i] = ok && k == k ? ordered(k) : 0;
-    }
-    if (g.groups > 1) {
-#pragma unroll
-        for (int i = 0; i < EPL; i++) skey[wave][lane + 64 * i] = key[i];
-        __builtin_amdgcn_wave_barrier();
-        uint64_t best = 0, second = 0;
-        if (lane < g.groups)
-            for (int i = 0; i < g.per_group; i++) {
-                const uint64_t k = skey[wave][lane * g.per_group + i];
-                if (k > best) {
-                    second = best;
-                    best = k;
-                } else if (k > second) {
-                    second = k;
-                }
+                for (int e = 0; e < V; e++) x[i + e] = in ? v[e] : -INFINITY;
             }
-        uint64_t rank_key = 0;   // of the sum of the group's largest keys
-        if (best) rank_key = ordered(unordered(best) + (g.group_top == 2 && second ? unordered(second) : 0.0));
-        int ahead = 0;
-        for (int j = 0; j < g.groups; j++) {
-            const uint64_t k = (uint64_t)__shfl((unsigned long long)rank_key, j, 64);
-            ahead += k > rank_key || (k == rank_key && j < lane) ? 1 : 0;
-        }
-        const uint64_t keep = __ballot(rank_key != 0 && ahead < g.topk_groups);
+        } else {
 #pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            const unsigned grp = ((unsigned)(lane + 64 * i) * g.group_mul) >> 20;
-            if (!((keep >> (grp & 63)) & 1)) key[i] = 0;
+            for (int i = 0; i < EPL; i++) x[i] = lane * EPL + i < g.E ? load_logit(g, row, lane * EPL + i) : -INFINITY;
+        }
+        float top = 0.f;
+        bool nan = false;
+        if (g.softmax) {
+            int m = KEY_NONE;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                m = x[i] == x[i] ? max(m, ordered(x[i])) : m;
+                nan |= x[i] != x[i];
+            }
+            m = wave_max(m);
+            top = m == KEY_NONE ? -INFINITY : unordered(m);
+            nan = __ballot(nan) != 0;
+        }
+        bool ok;
+        int mine = choose_f32<EPL>(x, g, nan ? INFINITY : top, (int *)lds[wave], lane, ok);
+        if (!ok) mine = choose_f64<EPL>(x, g, top, lds[wave], lane);
+        chosen[wave][lane] = mine;
+        if (g.softmax) {
+            if (!g.renorm) {
+                double sum = 0.0;
+#pragma unroll
+                for (int i = 0; i < EPL; i++) sum += lane * EPL + i < g.E ? exp((double)x[i] - (double)top) : 0.0;
+#pragma unroll
+                for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+                if (lane == 0) sums[wave] = sum;
+            }
+            if (lane == 0) tops[wave] = nan ? NAN : top;
         }
     }
-    int mine = -1;   // lane k's: the expert chosen k-th
-    for (int k = 0; k < g.topk; k++) {
-        uint64_t best = 0;
-        int at = -1;
-#pragma unroll
-        for (int i = 0; i < EPL; i++)
-            if (key[i] > best) {
-                best = key[i];
-                at = lane + 64 * i;
-            }
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) {
-            const uint64_t b = shfl_xor64(best, off);
-            const int a = __shfl_xor(at, off, 64);
-            if (b > best || (b == best && (unsigned)a < (unsigned)at)) {
-                best = b;
-                at = a;
-            }
+    __syncthreads();
+    const bool shared = g.topk <= 16;
+    if (shared && wave > 0) return;
+    const int r = shared ? lane >> 4 : wave, k = shared ? lane & 15 : lane;
+    const bool live = k < g.topk && row0 + r < g.rows;
+    const int mine = live ? chosen[r][k] : -1;
+    double w = 0.0;
+    if (mine >= 0) {
+        const double v = load_logit(g, row0 + r, mine);
+        if (g.softmax) {
+            w = exp(v - (double)tops[r]);
+            if (!g.renorm) w /= sums[r];
+        } else {
+            w = 1.0 / (1.0 + exp(-v));
         }
-        if (lane == k) mine = at;
-#pragma unroll
-        for (int i = 0; i < EPL; i++)
-            if (at == lane + 64 * i) key[i] = 0;
     }
-    double w = mine >= 0 ? score(load_logit(g, row, mine)) : 0.0;
     if (g.renorm) {
         double sum = w;
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+        for (int off = 1; off < g.topk; off <<= 1) sum += __shfl_xor(sum, off, 64);
         w = sum == 0.0 ? 0.0 : w / sum;
     }
-    if (lane < g.topk) {
-        g.ids[row * g.topk + lane] = mine;
-        g.weights[row * g.topk + lane] = (float)(w * (double)g.scale);
+    if (live) {
+        g.ids[(row0 + r) * g.topk + k] = mine;
+        g.weights[(row0 + r) * g.topk + k] = (float)(w * (double)g.scale);
     }
 }
 
@@ -770,6 +1015,14 @@ __global__ void __launch_bounds__(MOE_NT) moe_down_kernel(MoeArgs g) {
 
 }  // namespace
 
+template <int EPL>
+static int launch_route(const RouteArgs &g, hipStream_t stream) {
+    const dim3 grid((unsigned)((g.rows + 3) / 4)), block(256);
+    if (!g.bf16 && g.E % EPL == 0 && ((uintptr_t)g.logits & 15) == 0 && (EPL < 4 || g.E % 4 == 0))
+        return bs_enqueue(moe_route_kernel<EPL, true>, grid, block, stream, g);
+    return bs_enqueue(moe_route_kernel<EPL, false>, grid, block, stream, g);
+}
+
 int bs_launch_moe_route(RouteArgs g, hipStream_t stream) {
     constexpr int64_t ROWS = (int64_t)1 << 25;   // a launch holds fewer than 2^32 lanes
     const RouteArgs all = g;
@@ -778,12 +1031,11 @@ int bs_launch_moe_route(RouteArgs g, hipStream_t stream) {
         g.logits = (const uint8_t *)all.logits + first * all.E * (all.bf16 ? 2 : 4);
         g.ids = all.ids + first * all.topk;
         g.weights = all.weights + first * all.topk;
-        const dim3 grid((unsigned)((g.rows + 3) / 4)), block(256);
-        const int rc = g.E <= 64    ? bs_enqueue(moe_route_kernel<1>, grid, block, stream, g)
-                       : g.E <= 128 ? bs_enqueue(moe_route_kernel<2>, grid, block, stream, g)
-                       : g.E <= 256 ? bs_enqueue(moe_route_kernel<4>, grid, block, stream, g)
-                       : g.E <= 512 ? bs_enqueue(moe_route_kernel<8>, grid, block, stream, g)
-                                    : bs_enqueue(moe_route_kernel<16>, grid, block, stream, g);
+        const int rc = g.E <= 64    ? launch_route<1>(g, stream)
+                       : g.E <= 128 ? launch_route<2>(g, stream)
+                       : g.E <= 256 ? launch_route<4>(g, stream)
+                       : g.E <= 512 ? launch_route<8>(g, stream)
+                                    : launch_route<16>(g, stream);
         if (rc != 0) return rc;
     }
     return 0;
