@@ -855,8 +855,9 @@ __device__ __forceinline__ void tile_pieces(const v4f (&acc)[TM][TN], int i, boo
 // bands are contiguous (C is then plain row-major [M, N]): the epilogue of
 // such a tile takes the fast path of store_tile, and every lane issues all
 // 2 * TM of its stores.
+template <int COLS = BN>
 __device__ __forceinline__ bool tile_is_plain(const GemmArgs &g, int64_t m0, int64_t n0) {
-    return m0 + BM <= g.M && n0 + BN <= g.N && g.band_stride == g.band_rows * g.N;
+    return m0 + BM <= g.M && n0 + COLS <= g.N && g.band_stride == g.band_rows * g.N;
 }
 
 template <int MODE>
@@ -961,8 +962,12 @@ __device__ __forceinline__ u32x4 load_resid8(const ActArgs &q, int64_t at) {
 
 // A tile's accumulators in place of their results (GLU: in sub-tiles 0 and 1).  The
 // residual comes in the pieces of the store (tile_pieces), whole 128-byte row segments,
-// four row groups at a time, and goes to its columns' lanes by the same exchange.
-template <bool GLU>
+// BATCH row groups at a time, and goes to its columns' lanes by the same exchange.  Four
+// at a time: M = 16384, N = 7168, K = 2048 with a residual 266 us, against 270 for eight and
+// 273 for two, and 235 without bias, activation and residual.  What is left is the read of
+// the residual after the products, 235 MB or 44 us at the rate of a large copy, of which 13
+// are behind the tiles of other CUs.
+template <bool GLU, int BATCH>
 __device__ __forceinline__ void act_tile(v4f (&acc)[TM][TN], const GemmArgs &g, const ActArgs &q, int64_t m0,
                                          int64_t n0, int wm, int wn, int lane) {
     asm volatile("" : "+v"(lane));   // addresses formed here, not hoisted
@@ -974,59 +979,56 @@ __device__ __forceinline__ void act_tile(v4f (&acc)[TM][TN], const GemmArgs &g, 
     const BandOut o = GLU ? band_out(g, m0, n + 8 * fg, wm * WM + frow)
                           : band_out(g, m0, n + 8 * fg + (up ? 32 : 0), wm * WM + (lane & 7));
 #pragma unroll
-    for (int h = 0; h < TM; h += 4) {
-        u32x4 r[4][2] = {};
+    for (int h = 0; h < TM; h += BATCH) {
+        u32x4 r[BATCH][2] = {};
         if (q.resid) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < BATCH; i++) {
                 r[i][0] = load_resid8(q, band_at(g, o, (h + i) * 16, 0));
                 if (!GLU) r[i][1] = load_resid8(q, band_at(g, o, (h + i) * 16 + 8, up ? -32 : 32));
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < BATCH; i++) {
             v4f(&c)[TN] = acc[h + i];
-            float a[8], b[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                a[e] = c[e >> 2][e & 3];
-                b[e] = c[2 + (e >> 2)][e & 3];
-            }
-            add8(a, b0);
-            add8(b, b1);
-            u32x4 ra = {0u, 0u, 0u, 0u}, rb = ra;
+            u32x4 ra = r[i][0], rb = r[i][1];
             if (q.resid && !GLU) {
                 ra = up ? r[i][1] : r[i][0];
                 rb = swap_rows8(up ? r[i][0] : r[i][1]);
             }
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[e] = c[e >> 2][e & 3];
+            add8(v, b0);
+            act_all(v, q.act);
             if constexpr (GLU) {
-                act_all(a, q.act);
+                float u[8];
 #pragma unroll
-                for (int e = 0; e < 8; e++) a[e] *= b[e];
-                join8(a, r[i][0], q);
-            } else {
-                float v[16];
+                for (int e = 0; e < 8; e++) u[e] = c[2 + (e >> 2)][e & 3];
+                add8(u, b1);
 #pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    v[e] = a[e];
-                    v[8 + e] = b[e];
-                }
-                act_all(v, q.act);
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    a[e] = v[e];
-                    b[e] = v[8 + e];
-                }
-                join8(a, ra, q);
-                join8(b, rb, q);
+                for (int e = 0; e < 8; e++) v[e] *= u[e];
             }
+            join8(v, ra, q);
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                c[e >> 2][e & 3] = a[e];
-                if (!GLU) c[2 + (e >> 2)][e & 3] = b[e];
+            for (int e = 0; e < 8; e++) c[e >> 2][e & 3] = v[e];
+            if constexpr (!GLU) {
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[e] = c[2 + (e >> 2)][e & 3];
+                add8(v, b1);
+                act_all(v, q.act);
+                join8(v, rb, q);
+#pragma unroll
+                for (int e = 0; e < 8; e++) c[2 + (e >> 2)][e & 3] = v[e];
             }
         }
     }
+}
+
+// The lane's 8 columns of a gated row group.
+__device__ __forceinline__ u32x4 gated_piece(const v4f (&acc)[TM][TN], int i) {
+    return (u32x4){pack_bf16x2(acc[i][0][0], acc[i][0][1]), pack_bf16x2(acc[i][0][2], acc[i][0][3]),
+                   pack_bf16x2(acc[i][1][0], acc[i][1][1]), pack_bf16x2(acc[i][1][2], acc[i][1][3])};
 }
 
 // The gated tile's store: 64 bytes of 16 rows to an instruction.
@@ -1035,10 +1037,7 @@ __device__ __forceinline__ void store_gated_tile(const v4f (&acc)[TM][TN], const
     asm volatile("" : "+v"(lane));
     const BandOut o = band_out(g, m0, n0 + (wave & 3) * 32 + (lane >> 4) * 8, (wave >> 2) * WM + (lane & 15));
 #pragma unroll
-    for (int i = 0; i < TM; i++)
-        band_store<MODE_BS>(g, o, i * 16, 0,
-                            (u32x4){pack_bf16x2(acc[i][0][0], acc[i][0][1]), pack_bf16x2(acc[i][0][2], acc[i][0][3]),
-                                    pack_bf16x2(acc[i][1][0], acc[i][1][1]), pack_bf16x2(acc[i][1][2], acc[i][1][3])});
+    for (int i = 0; i < TM; i++) band_store<MODE_BS>(g, o, i * 16, 0, gated_piece(acc, i));
 }
 
 // ---- adapters --------------------------------------------------------------
@@ -1384,7 +1383,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
     if constexpr (LORA) {
         if (any) lora_add(acc, g, q, m0, n0 + wn * WN, wm, wave, lane);
     }
-    if constexpr (EPI != EPI_NONE) act_tile<GLU>(acc, g, ep, m0, n0, wm, wn, lane);
+    if constexpr (EPI != EPI_NONE) act_tile<GLU, 4>(acc, g, ep, m0, n0, wm, wn, lane);
     if constexpr (GLU) store_gated_tile(acc, g, m0, n0, wave, lane);
     else store_tile<MODE>(acc, g, m0, n0, wave, lane);
 }
@@ -1403,9 +1402,15 @@ struct PlainOffsets {
     uint32_t lx, ly;
     bool up;
 };
+template <bool GLU = false>
 __device__ __forceinline__ PlainOffsets plain_offsets(int64_t N, int wm, int wn, int lane) {
     asm volatile("" : "+v"(lane));   // formed here, per tile, not hoisted
     PlainOffsets o;
+    if constexpr (GLU) {   // one piece of the lane's row
+        o.lx = o.ly = (uint32_t)((wm * WM + (lane & 15)) * N + wn * 32 + (lane >> 4) * 8);
+        o.up = false;
+        return o;
+    }
     o.up = (lane >> 3) & 1;
     const int px = (lane >> 4) + (o.up ? 4 : 0);
     o.lx = (uint32_t)((wm * WM + (lane & 7)) * N + wn * WN + px * 8);
@@ -1417,8 +1422,13 @@ __device__ __forceinline__ PlainOffsets plain_offsets(int64_t N, int wm, int wn,
 // unrolled), stored non-temporally through rC (a descriptor of C from the
 // tile's first element on), or through the zero-size descriptor, which
 // stores nothing but issues the same two instructions.
+template <bool GLU = false>
 __device__ __forceinline__ void plain_store_rg(const v4f (&acc)[TM][TN], int i, __amdgpu_buffer_rsrc_t rC,
                                                int64_t N, const PlainOffsets &o) {
+    if constexpr (GLU) {
+        __builtin_amdgcn_raw_buffer_store_b128(gated_piece(acc, i), rC, 2 * ((uint32_t)(i * 16 * N) + o.lx), 0, 2);
+        return;
+    }
     u32x4 x, y;
     tile_pieces(acc, i, o.up, x, y);
     const uint32_t ri = (uint32_t)(i * 16 * N);   // the row group's first element
@@ -1459,8 +1469,8 @@ __device__ __forceinline__ void kblock_first(v4f (&acc)[TM][TN], v4f (&p)[4], Ta
         const v8i af = an;
         if (i + 1 < TM) an = lds_frag(as, wm * WM + (i + 1) * 16 + frow, fc);
         if (i == TM - 1) {
-            // vmcnt(2 * (7 - TAIL_RG)): the stores of row groups TAIL_RG..6 may remain
-            __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * (7 - TAIL_RG)));
+            // vmcnt: the stores of row groups TAIL_RG..6, two (GLU: one) to each, may remain
+            __builtin_amdgcn_s_waitcnt(0x0F70 | ((GLU ? 1 : 2) * (7 - TAIL_RG)));
             barrier_lds_only();
             a_next = lds_frag(stA<ST ^ 1>(), wm * WM + frow, fc);
             read_block_scales<ST ^ 1, GLU>(rn, wm, wn, frow);
@@ -1468,7 +1478,7 @@ __device__ __forceinline__ void kblock_first(v4f (&acc)[TM][TN], v4f (&p)[4], Ta
 #pragma unroll
         for (int j = 0; j < TN; j++) {
             const int k = i * TN + j;
-            if (j == 0 && i >= TAIL_RG) plain_store_rg(acc, i, rC, N, o);
+            if (j == 0 && i >= TAIL_RG) plain_store_rg<GLU>(acc, i, rC, N, o);
             if (j == 0 && i == TM - 1) {
                 // products 29..31 are first folded by the next block, which
                 // adds them (fma into the accumulator): start those at zero
@@ -1518,13 +1528,15 @@ __device__ __forceinline__ void kblock_first(v4f (&acc)[TM][TN], v4f (&p)[4], Ta
 // time (mxfp8).
 constexpr int DMA_SHIFT = 4;
 
-template <int MODE, int WMC, bool GLU = false>
+template <int MODE, int WMC, int EPI = EPI_NONE>
 __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
+    constexpr bool GLU = EPI == EPI_GLU;
+    constexpr int COLS = GLU ? BN / 2 : BN;
     constexpr int DSH = WMC == 1 ? DMA_SHIFT : 0;
     constexpr bool MX = MODE == MODE_MX;
     int vb = blockIdx.x;
     int64_t m0, n0;
-    if (!tile_of(g, vb, m0, n0)) return;
+    if (!tile_of<COLS>(g, vb, m0, n0)) return;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform: keep in SGPRs
@@ -1535,8 +1547,8 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
     const int fc = lane >> 4;   // the lane group: K chunks fc and fc + 4
 
     Loader L;
-    init_loader<MODE>(L, g, wave, lane);
-    L.P = whole_panels<MODE>(g, wave);
+    init_loader<MODE, GLU, true>(L, g, wave, lane);
+    L.P = whole_panels<MODE, GLU>(g, wave);
     shift_loader(L, tile_off<MODE>(g, m0, n0, wave));
 
     v4f acc[TM][TN];
@@ -1583,7 +1595,7 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
     TileOff dn = {0, 0, 0};
     auto find_next = [&]() {
         const GemmArgs gt = args();
-        has_next = __builtin_amdgcn_readfirstlane((int)tile_of(gt, vb + (int)gridDim.x, m0n, n0n));
+        has_next = __builtin_amdgcn_readfirstlane((int)tile_of<COLS>(gt, vb + (int)gridDim.x, m0n, n0n));
         dn = TileOff{0, 0, 0};
         if (has_next) {
             const TileOff tn = tile_off<MODE>(gt, m0n, n0n, wave), tc = tile_off<MODE>(gt, m0, n0, wave);
@@ -1605,7 +1617,7 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
         } else {
             {
                 const GemmArgs gt = args();
-                const PlainOffsets o = plain_offsets(gt.N, wm, wn, lane);
+                const PlainOffsets o = plain_offsets<GLU>(gt.N, wm, wn, lane);
                 const __amdgpu_buffer_rsrc_t rC =
                     pend ? make_rsrc(gt.C + pm0 * gt.N + pn0, (gt.M - pm0) * gt.N * 2) : L.rZ;
                 kblock_first<1>(acc, p, s_tail, a, bf, s, L, L.P, 1, true, wm, wn, frow, fc, rC,
@@ -1660,16 +1672,26 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
             // descriptor), so that the vector memory count of the next
             // tile's first block is exact.  The next tile's block 0 and its
             // head are already in (the last K block loaded them).
-            const bool plain = tile_is_plain(args(), m0, n0);
-            if (!has_next || !plain) store_tile<MODE>(acc, args(), m0, n0, wave, lane);
+            if constexpr (EPI != EPI_NONE) {
+                typedef const __attribute__((address_space(4))) ActGemmArgs *ActKArgs;
+                ActKArgs ka = (ActKArgs)gp;
+                asm volatile("" : "+s"(ka));
+                const ActGemmArgs at = *(const ActGemmArgs *)ka;
+                act_tile<GLU, 2>(acc, at.g, at.q, m0, n0, wm, wn, lane);
+            }
+            const bool plain = tile_is_plain<COLS>(args(), m0, n0);
+            if (!has_next || !plain) {
+                if constexpr (GLU) store_gated_tile(acc, args(), m0, n0, wave, lane);
+                else store_tile<MODE>(acc, args(), m0, n0, wave, lane);
+            }
             if (!has_next) break;
             {
                 const GemmArgs gt = args();
-                const PlainOffsets o = plain_offsets(gt.N, wm, wn, lane);
+                const PlainOffsets o = plain_offsets<GLU>(gt.N, wm, wn, lane);
                 const __amdgpu_buffer_rsrc_t rT =
                     plain ? make_rsrc(gt.C + m0 * gt.N + n0, (gt.M - m0) * gt.N * 2) : L.rZ;
 #pragma unroll
-                for (int i = 0; i < TAIL_RG; i++) plain_store_rg(acc, i, rT, gt.N, o);
+                for (int i = 0; i < TAIL_RG; i++) plain_store_rg<GLU>(acc, i, rT, gt.N, o);
             }
             pend = plain;
             pm0 = m0;
@@ -1686,6 +1708,11 @@ __global__ void __launch_bounds__(NTHREADS) bsgemm_persistent_kernel(GemmArgs g)
     // wm = wave / 4 = threadIdx.x / 256, the same for every lane of a wave
     if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8)) gemm_persistent<MODE_BS, 1>(g);
     else gemm_persistent<MODE_BS, 0>(g);
+}
+template <int EPI>
+__global__ void __launch_bounds__(NTHREADS) bsgemm_act_persistent_kernel(ActGemmArgs a) {
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8)) gemm_persistent<MODE_BS, 1, EPI>(a.g);
+    else gemm_persistent<MODE_BS, 0, EPI>(a.g);
 }
 __global__ void __launch_bounds__(NTHREADS) mxgemm_persistent_kernel(GemmArgs g) {
     gemm_persistent<MODE_MX, -1>(g);
@@ -1931,16 +1958,35 @@ __device__ __forceinline__ void mid_load(const MidLoader &L, int kb) {
                                              kb * 4, 0, 0);
 }
 
+// A wave's operands of one K block, in registers.
+struct MidBlock {
+    v8i a[2], b[2];
+    float s[2][2];
+};
+
+// b_scale of the K blocks from `first` on, one to a lane (of gate and up columns).
+// Loaded at each block they come between the blocks' DMA, and waiting for them is
+// waiting for all DMA on its way (0.65 us a block); so they are loaded for MID_RUN blocks
+// at a time.
+constexpr int MID_RUN = 63;   // a multiple of the stages, at most a wave's lanes
+struct MidScales {
+    int first;
+    float s[2];
+    __device__ __forceinline__ float at(int h, int kb) const {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, s[h]), kb - first));
+    }
+};
+
 template <int ST, bool GLU>
-__device__ __forceinline__ void mid_block(v4f (&acc)[2][2], const MidLoader &L, int kb, int KB, const float *sb,
-                                          const float *sb1, int lane) {
+__device__ __forceinline__ void mid_block(v4f (&acc)[2][2], const MidLoader &L, int kb, int KB, const MidScales &sb,
+                                          int lane) {
     const int frow = lane & 15, fg = lane >> 4, wm = L.wave >> 2, wn = L.wave & 3;
     __builtin_amdgcn_s_waitcnt(0x0F70 | (MID_DMA * (MID_STAGES - 2)));   // vmcnt: block kb is in
     barrier_lds_only();
     mid_load<(ST + MID_STAGES - 1) % MID_STAGES>(L, min(kb + MID_STAGES - 1, KB - 1));
     const uint8_t *st = stM<ST>();
     const float *sc = (const float *)(st + (MID_BM + MID_BN) * BK + L.wave * 256);
-    const float sbk = sb[kb], sbk1 = GLU ? sb1[kb] : 0.f;
+    const float sbk = sb.at(0, kb), sbk1 = GLU ? sb.at(1, kb) : 0.f;
     v8i a[2], b[2];
     float s[2][2];
 #pragma unroll
@@ -1987,18 +2033,31 @@ __device__ __forceinline__ void mid_sums(v4f (&acc)[2][2], const GemmArgs &g, in
         L.offB[i] = row * K + ((lane & 7) ^ (r & 7)) * 16;
     }
     L.offS = lane * KB * 4;
-    const float *sb = (const float *)g.sb + n0 / 128 * KB;
-    const float *sb1 = GLU ? sb + (int64_t)g.NB * KB : nullptr;
+    const float *sb = (const float *)g.sb + n0 / 128 * KB, *sb1 = sb + (int64_t)g.NB * KB;
+    MidScales b = {};
+    const auto scales = [&](int kb) {
+        const int k = min(kb + lane, KB - 1);
+        b.first = kb;
+        b.s[0] = sb[k];
+        if (GLU) b.s[1] = sb1[k];
+    };
+    scales(0);
 #pragma unroll
     for (int i = 0; i < 2; i++)
 #pragma unroll
         for (int j = 0; j < 2; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
     mid_load<0>(L, 0);
     mid_load<1>(L, min(1, KB - 1));
-    for (int kb = 0; kb < KB; kb += MID_STAGES) {
-        mid_block<0, GLU>(acc, L, kb, KB, sb, sb1, lane);
-        if (kb + 1 < KB) mid_block<1, GLU>(acc, L, kb + 1, KB, sb, sb1, lane);
-        if (kb + 2 < KB) mid_block<2, GLU>(acc, L, kb + 2, KB, sb, sb1, lane);
+    for (int kb = 0;;) {
+        const int end = min(kb + MID_RUN, KB);
+        for (; kb < end; kb += MID_STAGES) {
+            mid_block<0, GLU>(acc, L, kb, KB, b, lane);
+            if (kb + 1 < KB) mid_block<1, GLU>(acc, L, kb + 1, KB, b, lane);
+            if (kb + 2 < KB) mid_block<2, GLU>(acc, L, kb + 2, KB, b, lane);
+        }
+        if (kb >= KB) break;
+        scales(kb);
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0), so that the loop need not wait for them
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): the DMA past the last block is retired
 }
@@ -2078,90 +2137,130 @@ __global__ void __launch_bounds__(NTHREADS) bsgemm_act_mid_kernel(ActGemmArgs a)
 }
 
 // ---- few rows, with bias, activation and residual ------------------------------
-// At most 16 RG rows.  16 rows of B to a workgroup (GLU: 8 gate rows and the up rows
-// of the same columns), whose eight waves take the K blocks in turn: the whole weight
-// is in flight at once, where one wave for all of K waits for a few blocks at a
-// time.  The block products go to LDS, 8 U of them at a time, and are folded in
-// ascending order of K by a lane for each element, so the sums are those of the
-// other kernels bit for bit.
-template <int RG, int U, bool GLU>
+// 16 RG rows by 16 CT rows of B to a workgroup (GLU: of each 16, 8 gate rows and the up
+// rows of the same columns).  Its eight waves take the K blocks in turn, so that
+// all of a turn's loads are on their way together, where one wave for all of K waits for
+// a few blocks at a time.  The block products go to LDS, one of every wave's,
+// and are folded in ascending order of K by a lane for each four elements, so the sums
+// are those of the other kernels bit for bit.
+//
+// A weight's read bounds it.  M = 1, gated, N = 2048, K = 7168: 29 MB in 7.8 us, of which an
+// empty launch takes 3; M = 64,
+// N = 7168, K = 2048: 9.6 us, 16.7 MB.  The next turn's loads are on their way while one is
+// multiplied and folded; loads past the last turn, unused, cost what used ones do.
+template <int RG, int CT, bool GLU>
 __global__ void __launch_bounds__(NTHREADS) bsgemm_act_rows_kernel(ActGemmArgs a) {
-    constexpr int W = 8, COLS = GLU ? 8 : 16, SB = GLU ? 2 : 1;
-    constexpr int ELEMS = RG * 16 * COLS, PER = (ELEMS + NTHREADS - 1) / NTHREADS;
-    __shared__ v4f prod[W * U][RG][64];
-    __shared__ float scale[W * U][SB][RG * 16];
+    constexpr int W = 8, COLS = (GLU ? 8 : 16) * CT, UNITS = RG * CT * 64, PER = (UNITS + NTHREADS - 1) / NTHREADS;
+    constexpr int SB = GLU ? 2 : 1, SAS = (W * RG * 16 + NTHREADS - 1) / NTHREADS;
+    __shared__ v4f prod[2][W][CT][RG][64];
+    __shared__ float scale[2][W][SB][RG * 16];
     const GemmArgs &g = a.g;
     const ActArgs &q = a.q;
     const int tid = threadIdx.x, lane = tid & 63, frow = lane & 15, fg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t n0 = (int64_t)blockIdx.x * COLS, K = g.K;
-    const int KB = g.KB;
-    const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.A, g.M * K), rS = make_rsrc(g.sa, g.M * KB * 4);
-    const uint8_t *B = g.B + (GLU ? n0 + (frow & 7) + (frow >> 3) * g.N : n0 + frow) * K + 16 * fg;
+    const int64_t n0 = (int64_t)blockIdx.x * COLS, m0 = (int64_t)blockIdx.y * (16 * RG), K = g.K;
+    const int rows_in = (int)(g.M - m0 < 16 * RG ? g.M - m0 : 16 * RG);
+    const int KB = g.KB, turns = (KB + W - 1) / W;
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.A + m0 * K, rows_in * K);
+    const __amdgpu_buffer_rsrc_t rS = make_rsrc((const float *)g.sa + m0 * KB, (int64_t)rows_in * KB * 4);
+    const uint8_t *B[CT];
+#pragma unroll
+    for (int j = 0; j < CT; j++)
+        B[j] = g.B + (GLU ? n0 + 8 * j + (frow & 7) + (frow >> 3) * g.N : n0 + 16 * j + frow) * K + 16 * fg;
     const float *sb = (const float *)g.sb + n0 / 128 * KB, *sb1 = sb + (int64_t)g.NB * KB;
-    float acc[PER][SB] = {};
-    for (int k0 = 0; k0 < KB; k0 += W * U) {
-        v8i x[U][RG], b[U];
-        float s[U][RG];
+
+    v8i x[RG], b[CT];
+    float s[SAS], sbv[SAS][SB];
+    // nothing past the last block: a load costs the CU's 16 cycles even if it is not used
+    const auto load = [&](int t) {
+        const int kb = t * W + wave;
+        if (t >= turns) return;
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int kb = k0 + u * W + wave;
-            if (kb >= KB) break;
-            const u32x4 lo = __builtin_nontemporal_load((const u32x4 *)(B + (int64_t)kb * 128));
-            const u32x4 hi = __builtin_nontemporal_load((const u32x4 *)(B + (int64_t)kb * 128 + 64));
-            b[u] = (v8i){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+        for (int e = 0; e < SAS; e++) {   // the scales of one row and block of the turn
+            const int id = tid + e * NTHREADS, r = id / W, k = min(t * W + id % W, KB - 1);
+            s[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rS, (r * KB + k) * 4, 0, 0));
+            sbv[e][0] = sb[k];
+            if (GLU) sbv[e][SB - 1] = sb1[k];
+        }
+        if (kb >= KB) return;
 #pragma unroll
-            for (int i = 0; i < RG; i++) {
-                x[u][i] = frag_of(rA, (16 * i + frow) * (int)K + 16 * fg, kb * 128);
-                s[u][i] = __builtin_bit_cast(
-                    float, __builtin_amdgcn_raw_buffer_load_b32(rS, (16 * i + frow) * KB * 4, kb * 4, 0));
-            }
+        for (int j = 0; j < CT; j++) {
+            const u32x4 lo = *(const u32x4 *)(B[j] + (int64_t)kb * 128), hi = *(const u32x4 *)(B[j] + (int64_t)kb * 128 + 64);
+            b[j] = (v8i){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
         }
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int kb = k0 + u * W + wave;
-            if (kb >= KB) break;
-            const float sbk = GLU && fg >= 2 ? sb1[kb] : sb[kb];
+        for (int i = 0; i < RG; i++) x[i] = frag_of(rA, (16 * i + frow) * (int)K + 16 * fg, kb * 128);
+    };
+    v4f acc[PER];
 #pragma unroll
-            for (int i = 0; i < RG; i++) {
-                prod[u * W + wave][i][lane] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    b[u], x[u][i], (v4f){0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-                if (fg == 0 || (GLU && fg == 2)) scale[u * W + wave][fg >> 1][16 * i + frow] = s[u][i] * sbk;
+    for (int p = 0; p < PER; p++) acc[p] = (v4f){0.f, 0.f, 0.f, 0.f};
+    load(0);
+    for (int t = 0; t < turns; t++) {
+        const int buf = t & 1;
+#pragma unroll
+        for (int j = 0; j < CT; j++)
+#pragma unroll
+            for (int i = 0; i < RG; i++)
+                prod[buf][wave][j][i][lane] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    b[j], x[i], (v4f){0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < SAS; e++) {
+            const int id = tid + e * NTHREADS;
+            if (id < W * RG * 16) {
+#pragma unroll
+                for (int h = 0; h < SB; h++) scale[buf][id % W][h][id / W] = s[e] * sbv[e][h];
             }
         }
-        __syncthreads();
-        const int blocks = KB - k0 < W * U ? KB - k0 : W * U;
+        load(t + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        barrier_lds_only();   // and turn t - 1 is folded: its buffer is free for t + 1
+        const int blocks = min(KB - t * W, W);
 #pragma unroll
         for (int p = 0; p < PER; p++) {
             const int id = tid + p * NTHREADS;
-            if (id >= ELEMS) break;
-            // element e of lane l's four of row group i: row l % 16, row 4 (l / 16) + e of B's 16
-            const int i = id / (16 * COLS), l = id % (16 * COLS) / 4, e = id & 3;
-#pragma unroll 8
-            for (int k = 0; k < blocks; k++)
+            if (id >= UNITS) break;
+            const int i = (id >> 6) % RG, j = id / (64 * RG);
+            const int h = GLU ? fg >> 1 : 0;
+            if (blocks == W) {
 #pragma unroll
-                for (int h = 0; h < SB; h++)
-                    acc[p][h] = __builtin_fmaf(((const float *)&prod[k][i][l + 32 * h])[e], scale[k][h][16 * i + (l & 15)],
-                                               acc[p][h]);
+                for (int k = 0; k < W; k++)
+                    fold4(acc[p], prod[buf][k][j][i][lane], scale[buf][k][h][16 * i + frow]);
+            } else {
+                for (int k = 0; k < blocks; k++)
+                    fold4(acc[p], prod[buf][k][j][i][lane], scale[buf][k][h][16 * i + frow]);
+            }
         }
-        if (k0 + W * U < KB) __syncthreads();   // before the next products
     }
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
     for (int p = 0; p < PER; p++) {
         const int id = tid + p * NTHREADS;
-        if (id >= ELEMS) break;
-        const int i = id / (16 * COLS), l = id % (16 * COLS) / 4, e = id & 3;
-        const int m = 16 * i + (l & 15);
-        if (m >= g.M) continue;
-        const int64_t n = n0 + 4 * (l >> 4) + e;
-        float v[1] = {acc[p][0]};
-        if (q.bias) v[0] += bf16_lo(q.bias[n]);
+        if (id >= UNITS) break;   // whole waves
+        const int i = (id >> 6) % RG, j = id / (64 * RG), row = 16 * i + frow;
+        float v[4] = {acc[p][0], acc[p][1], acc[p][2], acc[p][3]}, u[4];
+        const int64_t n = n0 + (GLU ? 8 * j : 16 * j) + 4 * (GLU ? fg & 1 : fg);
+        if (q.bias) {
+            const u32x2 bv = *(const u32x2 *)(q.bias + n + (GLU && fg >= 2 ? g.N : 0));
+            v[0] += bf16_lo(bv[0]); v[1] += bf16_hi(bv[0]);
+            v[2] += bf16_lo(bv[1]); v[3] += bf16_hi(bv[1]);
+        }
+        if constexpr (GLU) {   // the up values of a lane's columns are 32 lanes on
+#pragma unroll
+            for (int e = 0; e < 4; e++) u[e] = __shfl_down(v[e], 32, 64);
+            if (fg >= 2) continue;
+        }
+        if (row >= rows_in) continue;
         act_all(v, q.act);
-        if constexpr (GLU) v[0] *= q.bias ? acc[p][1] + bf16_lo(q.bias[g.N + n]) : acc[p][1];
-        v[0] *= q.beta;
-        const int64_t at = element_at(g, (uint32_t)m, n);
-        if (q.resid) v[0] += q.alpha * bf16_lo(q.resid[at]);
-        g.C[at] = (uint16_t)pack_bf16x2(v[0], 0.f);
+        const int64_t at = element_at(g, (uint32_t)(m0 + row), n);
+        u32x2 r = {0u, 0u};
+        if (q.resid) r = *(const u32x2 *)(q.resid + at);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            if (GLU) v[e] *= u[e];
+            v[e] *= q.beta;
+            if (q.resid) v[e] += q.alpha * (e & 1 ? bf16_hi(r[e >> 1]) : bf16_lo(r[e >> 1]));
+        }
+        *(u32x2 *)(g.C + at) = (u32x2){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     }
 }
 
@@ -2254,10 +2353,10 @@ int bs_launch_gemm_lora(const uint8_t *A, const float *sa, const uint8_t *B, con
     // Short batches by waves of 16 x 32 or 32 x 64 while that takes at most two or one
     // of them to a CU, middling ones by 64 x 128 tiles while that takes at most two.
     // K = 2048, R = 16, us by graph launches, 16 x 32 / 32 x 64 / 64 x 128 / 256 x 256:
-    // N = 7168, M = 16: 9.0 / 12.8 / 13.4 / 27.0; M = 64: 19.3 / 13.9 / 15.5 / 28.5;
-    // M = 200: 50 / 34 / 15.5 / 32; M = 512: 112 / 57 / 22 / 34; M = 1024: 220 / 122 /
-    // 41 / 35; N = 1024, M = 256: 11.1 / 12.4 / 11.8 / 31; M = 512: 19.4 / 13.8 / 15.4 /
-    // 31; M = 2048: - / - / 16.9 / 27; M = 4096: - / - / 25 / 34.
+    // N = 7168, M = 16: 9.9 / 14.9 / 12.4 / 29; M = 64: 19.6 / 14.8 / 13.3 / 30;
+    // M = 200: 49 / 34 / 13.6 / 31; M = 512: 109 / 55 / 21 / 31; M = 1024: 216 / 122 /
+    // 39 / 32; N = 1024, M = 256: 11.0 / 12.3 / 11.1 / 29; M = 512: 19.0 / 12.8 / 11.6 /
+    // 29; M = 2048: - / - / 14.0 / 30; M = 4096: - / - / 23 / 30.
     const auto count = [&](int rows, int cols) { return N / cols * ((M + rows - 1) / rows); };
     const auto grid_of = [&](int rows, int cols) {
         return dim3((unsigned)((count(rows, cols) + NUM_XCD - 1) / NUM_XCD * NUM_XCD));
@@ -2271,11 +2370,25 @@ int bs_launch_gemm_lora(const uint8_t *A, const float *sa, const uint8_t *B, con
     return bs_enqueue(bsgemm_lora_tile_kernel, dim3(gemm_grid(g)), dim3(NTHREADS), stream, g, q);
 }
 
-template <int RG, int U>
+// Workgroups of the few-rows kernel in a column and in a row of them.
+static int64_t act_rows_x(const GemmArgs &g, bool gated, int CT) { return g.N / ((gated ? 8 : 16) * CT); }
+static int64_t act_rows_y(const GemmArgs &g, int RG) { return (g.M + 16 * RG - 1) / (16 * RG); }
+
+template <int RG, int CT>
 static int launch_act_rows(const ActGemmArgs &a, bool gated, hipStream_t stream) {
-    if (gated)
-        return bs_enqueue(bsgemm_act_rows_kernel<RG, U, true>, dim3((unsigned)(a.g.N / 8)), dim3(NTHREADS), stream, a);
-    return bs_enqueue(bsgemm_act_rows_kernel<RG, U, false>, dim3((unsigned)(a.g.N / 16)), dim3(NTHREADS), stream, a);
+    const dim3 grid((unsigned)act_rows_x(a.g, gated, CT), (unsigned)act_rows_y(a.g, RG));
+    if (gated) return bs_enqueue(bsgemm_act_rows_kernel<RG, CT, true>, grid, dim3(NTHREADS), stream, a);
+    return bs_enqueue(bsgemm_act_rows_kernel<RG, CT, false>, grid, dim3(NTHREADS), stream, a);
+}
+
+// Two of the 16 rows of B to a workgroup, which then reads A half as often, if that leaves
+// enough workgroups.  One / two, us: N = 7168, K = 2048 (448 of one): M = 1 6.2 / 5.9, M = 16
+// 7.5 / 6.5, M = 64 13.0 / 9.6; gated N = 2048, K = 7168 (256): M = 1 8.0 / 10.7, M = 16 10.1 /
+// 12.9, M = 64 19.8 / 22.6; N = 1024, K = 1024 (64): M = 1 3.5 / 4.0, M = 64 5.2 / 5.8.
+template <int RG>
+static int launch_act_rows(const ActGemmArgs &a, bool gated, hipStream_t stream) {
+    return act_rows_x(a.g, gated, 1) * act_rows_y(a.g, RG) >= 448 ? launch_act_rows<RG, 2>(a, gated, stream)
+                                                                   : launch_act_rows<RG, 1>(a, gated, stream);
 }
 
 int bs_launch_gemm_act(const uint8_t *A, const float *sa, const uint8_t *B, const float *sb, const uint16_t *bias,
@@ -2286,14 +2399,32 @@ int bs_launch_gemm_act(const uint8_t *A, const float *sa, const uint8_t *B, cons
     const ActGemmArgs a = {g, {bias, resid, alpha, beta, act}};
     const auto count = [&](int rows, int cols) { return N / cols * ((M + rows - 1) / rows); };
     const int mid_cols = gated ? MID_BN / 2 : MID_BN;
-    if (M <= 16) return g.KB <= 16 ? launch_act_rows<1, 2>(a, gated, stream) : launch_act_rows<1, 8>(a, gated, stream);
-    if (M <= 32) return launch_act_rows<2, 4>(a, gated, stream);
-    if (M <= 64) return launch_act_rows<4, 2>(a, gated, stream);
-    if (count(MID_BM, mid_cols) <= 512) {
+    const int64_t rows4 = act_rows_x(g, gated, 2) * act_rows_y(g, 4);
+    // Few rows by the kernel that splits K over a workgroup's waves, 16, 32 or 64 rows to
+    // one and the last while there is at most one of them to a CU; more by 64 x 128 tiles
+    // while that takes one row of them or at most two to a CU; else whole tiles.  us by graph
+    // launches, fewest rows that hold M / 64 rows / 64 x 128 / 256 x 256, with a residual,
+    // N = 7168, K = 2048: M = 16: 6.5 / 7.3 / 10.2 / 29; M = 32: 7.6 / 8.1 / 11.2 / 29; M = 64:
+    // 9.6 / 9.6 / 12.3 / 30; M = 128: - / 16.8 / 12.6 / 31; M = 512: - / 53 / 21 / 34; M =
+    // 1024: - / 102 / 37 / 35; gated, N = 2048, K = 7168: M = 16: 10.0 / 12.9 / 24 / 71; M =
+    // 128: - / 23 / 29 / 73; M = 256: - / 43 / 30 / 77; M = 512: - / 82 / 30 / 77; wide, K = 2048,
+    // M = 64: N = 28672: - / 30 / 13.8 / 28; N = 131072: - / - / 64 / 82 (M = 128: 93 / 86).
+    if (N < (int64_t)1 << 25) {   // a launch holds fewer than 2^32 lanes
+        if (M <= 16) return launch_act_rows<1>(a, gated, stream);
+        if (M <= 32) return launch_act_rows<2>(a, gated, stream);
+        if (rows4 <= 256) return launch_act_rows<4>(a, gated, stream);
+    }
+    if (M <= MID_BM || count(MID_BM, mid_cols) <= 512) {
         const dim3 grid((unsigned)((count(MID_BM, mid_cols) + NUM_XCD - 1) / NUM_XCD * NUM_XCD));
         return gated ? bs_enqueue(bsgemm_act_mid_kernel<true>, grid, dim3(NTHREADS), stream, a)
                      : bs_enqueue(bsgemm_act_mid_kernel<false>, grid, dim3(NTHREADS), stream, a);
     }
+    // The gated epilogue fits beside the persistent kernel's carried products (M = 16384,
+    // N = 2048: K = 2048 125 us against the tile kernel's 131, K = 7168 426 against 429); the
+    // plain one, with twice the columns to a lane, spilled 38 to 86 registers there.
+    const int64_t lim = 0x7FFFFFFF;   // as for bsgemm_fp8
+    if (gated && g.KB % 2 == 0 && (M + BM) * K <= lim && (2 * N + BN) * K <= lim)
+        return bs_enqueue(bsgemm_act_persistent_kernel<EPI_GLU>, dim3(persistent_grid(g, stream)), dim3(NTHREADS), stream, a);
     const dim3 grid(gemm_grid(g));
     return gated ? bs_enqueue(bsgemm_act_tile_kernel<EPI_GLU>, grid, dim3(NTHREADS), stream, a)
                  : bs_enqueue(bsgemm_act_tile_kernel<EPI_ACT>, grid, dim3(NTHREADS), stream, a);

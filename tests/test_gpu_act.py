@@ -67,7 +67,10 @@ SHAPES = [(1, 128, 128, 1, 0), (1, 2048, 1792, 1, 0), (3, 384, 2048, 3, 0), (16,
           (17, 256, 1152, 1, 0), (32, 384, 256, 4, 0), (33, 1152, 512, 3, 0), (64, 640, 2048, 8, 0),
           (65, 512, 256, 13, 5 * 512 + 16), (200, 384, 256, 4, 50 * 384 + 64), (257, 768, 1024, 1, 0),
           (513, 512, 1152, 1, 0), (700, 2176, 640, 7, 100 * 2176 + 8), (1537, 2304, 896, 1, 0), (2050, 2304, 128, 1, 0),
-          (2100, 2304, 384, 7, 0), (2600, 2560, 256, 8, 0), (2056, 2304, 512, 8, 257 * 2304 + 8), (2304, 2560, 512, 9, 0)]
+          (2100, 2304, 384, 7, 0), (2600, 2560, 256, 8, 0), (2056, 2304, 512, 8, 257 * 2304 + 8), (2304, 2560, 512, 9, 0),
+          (128, 256, 7168, 2, 0), (100, 7168, 256, 1, 0), (40, 7168, 128, 1, 0), (16, 7296, 256, 1, 0),
+          (300, 128, 8320, 3, 0), (70, 2304, 8192, 1, 0),
+          (50, 66048, 128, 5, 0)]
 
 
 @pytest.mark.parametrize("M,N,K,bands,stride", SHAPES)
@@ -218,3 +221,24 @@ def test_weight_past_32_bits():
         assert bool((got == want).all()), M
         got = bs.bsgemm_fp8_act(A[:M], sa[:M], B, sb).view(M, 2 * N)
         assert bool((got == t.to(torch.bfloat16)).all()), M
+
+
+def test_millions_of_columns():
+    """More columns than the few-rows kernel's grid holds, and just fewer."""
+    say("bsgemm_fp8_act millions of columns")
+    for N in ((1 << 25) - 256, 1 << 25):
+        K = 128
+        B = torch.zeros((N, K), dtype=torch.uint8, device=device())
+        B[:, 5] = 0x38
+        B[N - 1, 5] = 0x40
+        sb = (torch.arange(N // 128, device=device()) % 4 + 1).to(torch.float32).view(-1, 1)
+        A = torch.zeros((3, K), dtype=torch.uint8, device=device())
+        A[:, 5] = torch.tensor([0x38, 0x40, 0xB8], dtype=torch.uint8, device=device())   # 1, 2, -1
+        sa = torch.ones((3, 1), dtype=torch.float32, device=device())
+        want = sb.view(-1).repeat_interleave(128)
+        want[N - 1] *= 2
+        C = bs.bsgemm_fp8_act(A, sa, B, sb, act="relu").view(3, N)
+        assert bool((C[0] == want).all()) and bool((C[1] == 2 * want).all()) and bool((C[2] == 0).all())
+        half = N // 2
+        C = bs.bsgemm_fp8_act(A, sa, B, sb, gated=True).view(3, half)
+        assert bool((C[0] == want[:half] * want[half:]).all())
