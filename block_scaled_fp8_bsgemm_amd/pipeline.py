@@ -21,11 +21,14 @@ captured.
 ``WoBServeStep`` is the same layer as a serving stack runs it: a bf16 input, low-rank
 adapters of many requests beside the weight, and the gathered wire taken
 straight into the residual stream and the next projection's fp8 operand.
+
+``FFNServeStep`` is the feed-forward block that takes over there: the dense or shared
+part as two products with their epilogues, and the routed experts of a few tokens.
 """
 import torch
 
-from . import (actq_e4m3, band_reduce, band_rowq_e4m3, bsgemm_fp8, bsgemm_fp8_lora, lora_expand, lora_plan,
-               lora_shrink, resnorm, rowdq_e4m3, rowq_e4m3)
+from . import (actq_e4m3, band_reduce, band_rowq_e4m3, bsgemm_fp8, bsgemm_fp8_act, bsgemm_fp8_lora, lora_expand,
+               lora_plan, lora_shrink, moe_fp8, moe_fp8_workspace, moe_route, resnorm, rowdq_e4m3, rowq_e4m3)
 
 
 class WoBStep:
@@ -156,6 +159,88 @@ class WoBServeStep:
     def norm(self):
         resnorm(self.wire_q, self.resid, y_scale=self.wire_s, resid_out=self.resid_out, z=self.z, q=self.q,
                 q_scale=self.q_scale, **self.norm_args)
+
+    def step(self):
+        for ph in self.PHASES:
+            getattr(self, ph)()
+
+
+class FFNServeStep:
+    """One feed-forward block on resnorm's outputs, z (bf16) and q with q_scale (fp32 per
+    1x128 block):
+
+      1. up          h = act(q W1^T) * (q W3^T), the dense part (a layer's only expert or the
+                     one that all tokens share): bsgemm_fp8_act, gated
+      2. quantize    h -> the second product's fp8 operand (actq_e4m3)
+      3. down        out = h W2^T (bsgemm_fp8_act)
+      4. logits      z router^T in fp32: lora_shrink with the router as every row's adapter
+      5. route       each token's experts and weights (moe_route)
+      6. experts     out += the experts' weighted outputs (moe_fp8)
+
+    Without a dense part 4 to 6 alone, which need no q; without a router 1 to 3 alone, for any
+    number of rows, which need no z.  Experts: up to 128 rows.  The next resnorm takes out as
+    its y.  z, q and q_scale may be refilled between steps: every buffer is allocated here
+    and step() only enqueues, so it can be captured.
+    """
+
+    DENSE, ROUTED = ("up", "quantize", "down"), ("logits", "route", "experts")
+
+    def __init__(self, z=None, q=None, q_scale=None, dense=None, router=None, experts=None, topk=1, act="silu",
+                 bias=None, **route):
+        """z bf16 [M, D]; q uint8 [M, D], q_scale fp32 [M, D/128]; dense: (B13, s13, B2, s2), the weight
+        [2I, D], W1's rows first, and [D, I] with their scales, or None; router: bf16 [E, D], E a
+        multiple of 8 up to 256, with experts: (W13, s13, W2, s2) as for moe_fp8, or None;
+        topk, bias and route (score, groups, ...): as for moe_route."""
+        if (router is None) != (experts is None):
+            raise ValueError("router and experts go together")
+        if dense is None and experts is None:
+            raise ValueError("need a dense part, experts or both")
+        if dense is not None and (q is None or q_scale is None):
+            raise ValueError("the dense part needs q and q_scale")
+        if experts is not None and z is None:
+            raise ValueError("the experts need z")
+        M, D = (q if z is None else z).shape
+        dev = (q if z is None else z).device
+
+        def new(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        self.z, self.q, self.q_scale, self.act, self.topk = z, q, q_scale, act, topk
+        self.dense, self.router, self.expert_weights, self.bias, self.route_args = dense, router, experts, bias, route
+        self.out = new((M, D), torch.bfloat16)
+        self.PHASES = (self.DENSE if dense is not None else ()) + (self.ROUTED if experts is not None else ())
+        if dense is not None:
+            I = dense[2].shape[1]
+            self.h = new((M, I), torch.bfloat16)
+            self.hq, self.h_scale = new((M, I), torch.uint8), new((M, I // 128), torch.float32)
+        if experts is not None:
+            E, rows = experts[0].shape[:2]
+            if router.shape[0] != E:
+                raise ValueError(f"the router has {router.shape[0]} experts, the weights {E}")
+            self.router = router.view(1, E, D)
+            self.plan = lora_plan(torch.zeros(M, dtype=torch.int32, device=dev), 1)
+            self.router_logits = new((M, E), torch.float32)
+            self.ids, self.weights = new((M, topk), torch.int32), new((M, topk), torch.float32)
+            self.ws = new(moe_fp8_workspace(M, topk, E, rows // 2), torch.uint8)
+
+    def up(self):
+        bsgemm_fp8_act(self.q, self.q_scale, *self.dense[:2], act=self.act, gated=True, C=self.h)
+
+    def quantize(self):
+        actq_e4m3(self.h, self.hq, self.h_scale)
+
+    def down(self):
+        bsgemm_fp8_act(self.hq, self.h_scale, *self.dense[2:], C=self.out)
+
+    def logits(self):
+        lora_shrink(self.z, self.router, self.plan, self.router_logits)
+
+    def route(self):
+        moe_route(self.router_logits, self.topk, bias=self.bias, ids=self.ids, weights=self.weights, **self.route_args)
+
+    def experts(self):
+        moe_fp8(self.z, self.ids, self.weights, *self.expert_weights, base=None if self.dense is None else self.out,
+                act=self.act, out=self.out, ws=self.ws)
 
     def step(self):
         for ph in self.PHASES:

@@ -191,3 +191,19 @@ def test_reference_act():
     x = np.linspace(-6, 6, 4001)
     for name in ffnref.ACTS:
         assert np.max(np.abs(np.diff(ffnref.act(x, name)))) <= ffnref.SLOPE * (x[1] - x[0]) * 1.0001, name
+
+
+def test_step_refusals():
+    from block_scaled_fp8_bsgemm_amd.pipeline import FFNServeStep
+    z = torch.zeros((4, 256), dtype=torch.bfloat16)
+    q, qs = torch.zeros((4, 256), dtype=torch.uint8), torch.ones((4, 2))
+    dense = (torch.zeros((256, 256), dtype=torch.uint8), torch.ones((2, 2)),
+             torch.zeros((256, 128), dtype=torch.uint8), torch.ones((2, 1)))
+    experts = tuple(t.expand(8, *t.shape).contiguous() for t in dense)
+    router = torch.zeros((8, 256), dtype=torch.bfloat16)
+    for kw, message in ((dict(z=z, q=q, q_scale=qs), "need a dense part"), (dict(z=z, router=router), "go together"),
+                        (dict(z=z, experts=experts), "go together"), (dict(z=z, dense=dense), "needs q"),
+                        (dict(q=q, q_scale=qs, router=router, experts=experts), "need z"),
+                        (dict(z=z, router=router[:4], experts=experts), "4 experts")):
+        with pytest.raises(ValueError, match=message):
+            FFNServeStep(**kw)
