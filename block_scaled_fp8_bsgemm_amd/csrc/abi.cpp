@@ -421,7 +421,7 @@ extern "C" {
 bs_status moe_fp8_workspace(int64_t M, int64_t topk, int64_t E, int64_t I, int64_t *bytes) {
     if (!bytes) return BS_ERR_INVALID;
     if (const bs_status st = moe_dims(M, topk, E, I); st != BS_OK) return st;
-    *bytes = bs_moe_workspace(M, topk, I);
+    *bytes = bs_moe_workspace(M, topk, E, I);
     return BS_OK;
 }
 
@@ -443,11 +443,11 @@ bs_status moe_fp8(const uint16_t *x, const int32_t *ids, const float *weights, c
     const Range in[] = {range_of(x, M * D * 2), range_of(ids, M * topk * 4), range_of(weights, M * topk * 4),
                         range_of(W13, 2 * E * I * D), range_of(s13, 2 * blocks * 4), range_of(W2, E * I * D),
                         range_of(s2, blocks * 4), range_of(base, base ? M * D * 2 : 0)};
-    const Range ro = range_of(out, M * D * 2), rws = range_of(ws, bs_moe_workspace(M, topk, I));
+    const Range ro = range_of(out, M * D * 2), rws = range_of(ws, bs_moe_workspace(M, topk, E, I));
     if (overlap(ro, rws)) return BS_ERR_INVALID;
     for (int i = 0; i < 8; i++)
         if (overlap(rws, in[i]) || (overlap(ro, in[i]) && !(i == 7 && base == out))) return BS_ERR_INVALID;
-    const MoeArgs g = {x, ids, weights, W13, s13, W2, s2, base, out, (uint16_t *)ws, (int)M, (int)topk, (int)E, act, D, I};
+    const MoeArgs g = {x, ids, weights, W13, s13, W2, s2, base, out, (uint16_t *)ws, nullptr, (int)M, (int)topk, (int)E, act, D, I};
     return bs_launch_moe(g, as_stream(stream)) == 0 ? BS_OK : BS_ERR_LAUNCH;
 }
 

@@ -97,10 +97,11 @@ struct MoeArgs {
     const uint16_t *base;   // bf16 [M, D] or null
     uint16_t *out;          // bf16 [M, D]
     uint16_t *h;            // workspace: bf16 [M * topk, I / 16, 2, 16], high and low parts
+    float *part;            // and behind it fp32 [classes, M, D] (set by the launch)
     int M, topk, E, act;
     int64_t D, I;
 };
-int64_t bs_moe_workspace(int64_t M, int64_t topk, int64_t I);
+int64_t bs_moe_workspace(int64_t M, int64_t topk, int64_t E, int64_t I);
 int bs_launch_moe(const MoeArgs &g, hipStream_t stream);
 int bs_stream_cus(hipStream_t stream);   // CUs of the stream's device
 

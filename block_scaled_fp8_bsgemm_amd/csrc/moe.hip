@@ -458,7 +458,10 @@ struct MoeLists {
 // the first, with the sum of their weights.  The tokens of an expert stand in the order
 // that its counter gave them, which no result depends on: a token has its own column
 // of an MFMA, and its own sums.
-__device__ __forceinline__ void moe_lists(MoeLists &l, int *scratch, const MoeArgs &g, bool weights) {
+//
+// Of the experts whose number is `rest` modulo `classes` alone.
+__device__ __forceinline__ void moe_lists(MoeLists &l, int *scratch, const MoeArgs &g, bool weights, int classes,
+                                          int rest) {
     int *ids = scratch, *hist = ids + MOE_PAIRS, *total = hist + MOE_PAIRS;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, pairs = g.M * g.topk;
 #pragma unroll
@@ -467,7 +470,7 @@ __device__ __forceinline__ void moe_lists(MoeLists &l, int *scratch, const MoeAr
         hist[i] = 0;
         if (i < pairs) {
             const int e = g.ids[i];
-            ids[i] = (unsigned)e < (unsigned)g.E ? e : -1;
+            ids[i] = (unsigned)e < (unsigned)g.E && e % classes == rest ? e : -1;
         }
     }
     __syncthreads();
@@ -798,7 +801,7 @@ __device__ __forceinline__ bool up_stage(v4f (&acc)[2][G], UpRegs<G> (&r)[2], Up
 template <int G>
 __global__ void __launch_bounds__(MOE_NT) moe_up_kernel(MoeArgs g) {
     __shared__ MoeLists l;
-    moe_lists(l, (int *)slot_of<0>(0), g, false);
+    moe_lists(l, (int *)slot_of<0>(0), g, false, 1, 0);
     UpWork w;
     w.l = &l;
     w.lane = threadIdx.x & 63;
@@ -959,12 +962,23 @@ __device__ __forceinline__ bool down_stage(v4f (&acc)[T][DG], DownRegs<T> (&r)[2
     return a.t < w.count;
 }
 
+// base + v as four elements of out.
+__device__ __forceinline__ void moe_store(const MoeArgs &g, int64_t at, v4f v) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    if (g.base) {
+        const u32x2 b = *(const u32x2 *)(g.base + at);
+        v[0] += bf16_lo(b[0]); v[1] += bf16_hi(b[0]);
+        v[2] += bf16_lo(b[1]); v[3] += bf16_hi(b[1]);
+    }
+    *(u32x2 *)(g.out + at) = (u32x2){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
 template <int T, int MMAX>
 __global__ void __launch_bounds__(MOE_NT) moe_down_kernel(MoeArgs g) {
     __shared__ MoeLists l;
     __shared__ v4f sum[MOE_WAVES][MMAX * 4 * T];
     for (int i = threadIdx.x; i < MOE_WAVES * MMAX * 4 * T; i += MOE_NT) sum[0][i] = (v4f){0.f, 0.f, 0.f, 0.f};
-    moe_lists(l, (int *)slot_of<0>(0), g, true);
+    moe_lists(l, (int *)slot_of<0>(0), g, true, (int)gridDim.y, (int)blockIdx.y);
     DownWork w;
     w.l = &l;
     w.lane = threadIdx.x & 63;
@@ -1003,14 +1017,19 @@ __global__ void __launch_bounds__(MOE_NT) moe_down_kernel(MoeArgs g) {
 #pragma unroll
         for (int k = 0; k < MOE_WAVES; k++) v += sum[k][m * 4 * T + (c ^ (m & 3))];
         const int64_t at = m * g.D + w.n0 + 4 * c;
-        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-        if (g.base) {
-            const u32x2 b = *(const u32x2 *)(g.base + at);
-            v[0] += bf16_lo(b[0]); v[1] += bf16_hi(b[0]);
-            v[2] += bf16_lo(b[1]); v[3] += bf16_hi(b[1]);
-        }
-        *(u32x2 *)(g.out + at) = (u32x2){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        if (gridDim.y > 1) *(v4f *)(g.part + (int64_t)blockIdx.y * g.M * g.D + at) = v;
+        else moe_store(g, at, v);
     }
+}
+
+// The classes' sums, in their order.
+__global__ void __launch_bounds__(64) moe_join_kernel(MoeArgs g, int classes) {
+    const int64_t n = g.M * g.D, at = ((int64_t)blockIdx.x * 64 + threadIdx.x) * 4;
+    if (at >= n) return;
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int k = 0; k < classes; k++) v += *(const v4f *)(g.part + k * n + at);
+    moe_store(g, at, v);
 }
 
 }  // namespace
@@ -1041,23 +1060,38 @@ int bs_launch_moe_route(RouteArgs g, hipStream_t stream) {
     return 0;
 }
 
-// h: 32 bits for each of its values, of every pair.
-int64_t bs_moe_workspace(int64_t M, int64_t topk, int64_t I) { return 4 * M * topk * I; }
-
-template <int T, int MMAX>
-static int launch_down(const MoeArgs &g, hipStream_t stream) {
-    return bs_enqueue(moe_down_kernel<T, MMAX>, dim3((unsigned)(g.D / (16 * T))), dim3(MOE_NT), stream, g);
+// Classes that the experts are split into by their numbers, each with workgroups of its
+// own: with few columns the workgroups are few, and each takes about 1 us an expert.
+constexpr int CLASS_COLUMNS = 8192;   // about 256 workgroups of 32 columns
+static int moe_classes(int64_t E, int64_t D) {
+    const int64_t most = (E + 1) / 2, c = CLASS_COLUMNS / D;   // two experts to a class
+    return (int)(c < 1 || most < 1 ? 1 : c < most ? c : most);
 }
 
-int bs_launch_moe(const MoeArgs &g, hipStream_t stream) {
+// h: 32 bits for each of its values, of every pair; then each class's sums, fp32 [M, D].
+int64_t bs_moe_workspace(int64_t M, int64_t topk, int64_t E, int64_t I) {
+    return 4 * M * topk * I + (E > 2 ? 4 * CLASS_COLUMNS * M : 0);
+}
+
+template <int T, int MMAX>
+static int launch_down(const MoeArgs &g, int classes, hipStream_t stream) {
+    return bs_enqueue(moe_down_kernel<T, MMAX>, dim3((unsigned)(g.D / (16 * T)), (unsigned)classes), dim3(MOE_NT), stream, g);
+}
+
+int bs_launch_moe(const MoeArgs &args, hipStream_t stream) {
+    MoeArgs g = args;
+    g.part = (float *)(g.h + 2 * (int64_t)g.M * g.topk * g.I);
     const int64_t slots = g.E < g.M * g.topk ? g.E : g.M * g.topk, items = slots * (g.I / 16);
     const int64_t wgs = 2 * (int64_t)bs_stream_cus(stream);
     const dim3 up((unsigned)(items < wgs ? items : wgs)), block(MOE_NT);
-    const int rc = g.M <= 16 ? bs_enqueue(moe_up_kernel<2>, up, block, stream, g)
-                             : bs_enqueue(moe_up_kernel<4>, up, block, stream, g);
+    int rc = g.M <= 16 ? bs_enqueue(moe_up_kernel<2>, up, block, stream, g)
+                       : bs_enqueue(moe_up_kernel<4>, up, block, stream, g);
     if (rc != 0) return rc;
     // 32 columns to a workgroup while its waves' sums of all tokens fit beside the slots
-    return g.M <= 16   ? launch_down<2, 16>(g, stream)
-           : g.M <= 64 ? launch_down<2, 64>(g, stream)
-                       : launch_down<1, 128>(g, stream);
+    const int classes = moe_classes(g.E, g.D);
+    rc = g.M <= 16   ? launch_down<2, 16>(g, classes, stream)
+         : g.M <= 64 ? launch_down<2, 64>(g, classes, stream)
+                     : launch_down<1, 128>(g, classes, stream);
+    if (rc != 0 || classes == 1) return rc;
+    return bs_enqueue(moe_join_kernel, dim3((unsigned)((g.M * g.D / 4 + 63) / 64)), dim3(64), stream, g, classes);
 }
