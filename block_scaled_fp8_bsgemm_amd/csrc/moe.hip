@@ -409,9 +409,9 @@ __global__ void __launch_bounds__(256) moe_route_kernel(RouteArgs g) {
 // The weights come by DMA into two slots of LDS for each wave, 32 rows x 128 bytes (or 16 x
 // 256) to a slot, and the other operand to registers, also for one slot ahead: a wave multiplies
 // one slot while the next is on its way, through the boundaries of items too, and
-// waits for its own loads alone, by their number.  Every load is issued whether or not
-// there is something to load, then out of its descriptor's range, so that the number
-// is always the same.
+// waits for its own loads alone, by their number.  A wave with a share issues every load
+// whether or not there is something to load, then out of its descriptor's range, so that
+// the number is known where they are waited for; one without a share loads nothing.
 
 constexpr int MOE_WAVES = 8, MOE_NT = MOE_WAVES * 64;
 constexpr int MOE_PAIRS = 1024;      // most M * topk, and most experts
@@ -463,6 +463,7 @@ struct MoeLists {
 __device__ __forceinline__ void moe_lists(MoeLists &l, int *scratch, const MoeArgs &g, bool weights, int classes,
                                           int rest) {
     int *ids = scratch, *hist = ids + MOE_PAIRS, *total = hist + MOE_PAIRS;
+    float *given = (float *)(total + MOE_WAVES);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, pairs = g.M * g.topk;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
@@ -470,6 +471,7 @@ __device__ __forceinline__ void moe_lists(MoeLists &l, int *scratch, const MoeAr
         hist[i] = 0;
         if (i < pairs) {
             const int e = g.ids[i];
+            if (weights) given[i] = g.weights[i];
             ids[i] = (unsigned)e < (unsigned)g.E && e % classes == rest ? e : -1;
         }
     }
@@ -516,17 +518,18 @@ __device__ __forceinline__ void moe_lists(MoeLists &l, int *scratch, const MoeAr
         if (weights) {
             float w = 0.f;
             for (int k = i; k < (m + 1) * g.topk; k++)
-                if (ids[k] == mine[j]) w += g.weights[k];
+                if (ids[k] == mine[j]) w += given[k];
             l.w[pos] = w;
         }
     }
     __syncthreads();
 }
 
-// A wave's share of `units` pieces of 64, and the slots that the largest share fills.
-__device__ __forceinline__ int share(int units, int wave) { return units * wave / MOE_WAVES; }
-template <int T> __device__ __forceinline__ int stages_of(int units) {
-    return ((units + MOE_WAVES - 1) / MOE_WAVES + SU<T> - 1) / SU<T>;
+// Where a wave's share of `blocks` 128 deep blocks begins, in units of 64, and the slots that the
+// largest share fills.  With fewer blocks than waves some have none, and load nothing.
+__device__ __forceinline__ int share(int blocks, int wave) { return blocks * wave / MOE_WAVES * 2; }
+template <int T> __device__ __forceinline__ int stages_of(int blocks) {
+    return ((blocks + MOE_WAVES - 1) / MOE_WAVES * 2 + SU<T> - 1) / SU<T>;
 }
 
 // T tiles of 16 rows of `pitch` bytes each.
@@ -625,6 +628,12 @@ template <int Z> __device__ __forceinline__ v4f add_pieces(v4f v) {
     return v;
 }
 
+// Units of stage `a`, an even number.
+template <int T, typename At, typename Work>
+__device__ __forceinline__ int units_of(const At &a, const Work &w) {
+    return a.n > 0 ? min(max(w.end - (w.first + a.k * SU<T>), 0), SU<T>) : 0;
+}
+
 // All loads of a stage but the next one's are done: those are `groups` for each unit, the
 // scales and the slot's.
 template <int T, int MAX>
@@ -692,7 +701,7 @@ __device__ __forceinline__ void up_next(UpAt<G> &a, const UpWork &w, int64_t D) 
 
 template <int G> struct UpRegs {
     v8bf x[2][G];
-    float sc;   // lane 8 h + q: the scale of unit q, tile h
+    float sc;   // lane h: the scale of the block, tile h
 };
 
 // Loads of stage `a` into slot ST and r.
@@ -701,19 +710,18 @@ __device__ __forceinline__ void up_load(UpRegs<G> &r, const UpAt<G> &a, const Up
                                         const LaneOffsets<2> &o) {
     const int64_t row = (int64_t)a.expert * 2 * g.I + a.c0;
     const int u0 = w.first + a.k * SU<2>;
-    const int units = a.n > 0 ? min(max(w.end - u0, 0), SU<2>) : 0;
+    const int units = units_of<2>(a, w);
 #pragma unroll
     for (int i = 0; i < G; i++) {
         if (i >= a.groups) break;
 #pragma unroll
         for (int q = 0; q < SU<2>; q++)
-            r.x[q][i] = load_v8(w.x, q < units ? a.off[i] : OUT_OF_RANGE, (u0 + q) * 128);
+            r.x[q][i] = load_v8(w.x, units ? a.off[i] : OUT_OF_RANGE, (u0 + q) * 128);
     }
     const int64_t DB = g.D / 128;
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(g.s13 + row / 128 * DB, (g.I / 128 * DB + DB) * 4);
-    const int q = w.lane & 7, h = w.lane >> 3;
     r.sc = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                         rs, h < 2 && q < units ? ((int)(h * g.I / 128 * DB) + (u0 + q) / 2) * 4 : OUT_OF_RANGE, 0, 0));
+                                         rs, w.lane < units ? (w.lane * (int)(g.I / 128 * DB) + u0 / 2) * 4 : OUT_OF_RANGE, 0, 0));
     const Tiles<2> t = {make_rsrc(g.W13 + row * g.D, 16 * g.D), make_rsrc(g.W13 + (row + g.I) * g.D, 16 * g.D)};
     moe_dma<ST, 2>(t, o, u0, units, w.wave);
 }
@@ -723,45 +731,49 @@ __device__ __forceinline__ void up_load(UpRegs<G> &r, const UpAt<G> &a, const Up
 // their low parts.
 template <int G, int ST>
 __device__ __forceinline__ void up_finish(const v4f (&acc)[2][G], const UpAt<G> &a, const UpWork &w, const MoeArgs &g) {
-    constexpr int GP = 2;   // groups at a time: a slot holds four of a wave's tiles
-    static_assert(G % GP == 0, "whole turns");
+    constexpr int TP = (G + 1) / 2;   // tiles of two groups: even lanes have one's rows, odd lanes the other's
+    static_assert(2 * TP * 1024 <= SLOT, "a wave's tiles fit a slot");
+    v4f *own = (v4f *)slot_of<ST>(w.wave);
 #pragma unroll
-    for (int i0 = 0; i0 < G; i0 += GP) {
-        if (i0 >= a.groups) break;
-        v4f *own = (v4f *)slot_of<ST>(w.wave);
+    for (int j = 0; j < TP; j++) {
+        if (2 * j >= a.groups) break;
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+        for (int h = 0; h < 2; h++) {
+            const v4f even = add_pieces<2>(acc[h][2 * j]), odd = add_pieces<2>(acc[h][2 * j + 1]);
+            v4f v;
 #pragma unroll
-            for (int i = 0; i < GP; i++) own[(h * GP + i) * 64 + w.lane] = acc[h][i0 + i];
-        barrier_lds_only();
-        const int i = (w.wave - a.it) & (MOE_WAVES - 1);   // another wave from item to item
-        if (i < GP && i0 + i < a.groups) {
-            const int row = a.r0 + 8 * (i0 + i) + (w.fr >> 1);
-            v4f t[2];
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                t[h] = (v4f){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int v = 0; v < MOE_WAVES; v++)
-                    t[h] += ((const v4f *)slot_of<ST>(v))[(h * GP + i) * 64 + w.lane];
-                t[h] = add_pieces<2>(t[h]);
-            }
-            float v[4] = {t[0][0], t[0][1], t[0][2], t[0][3]};
-            act_all(v, g.act);
-            if (row < a.n) {   // even lanes the high parts, odd ones the low parts
-                typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-                v4bf part;
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    const float h = v[q] * t[1][q];
-                    const __bf16 hi = (__bf16)h;
-                    part[q] = w.fr & 1 ? (__bf16)(h - (float)hi) : hi;
-                }
-                *(v4bf *)(g.h + ((int64_t)(w.l->at[a.first + row] >> 8) * g.I + a.c0) * 2 + 16 * (w.fr & 1) + 4 * w.fg) = part;
-            }
+            for (int e = 0; e < 4; e++) v[e] = w.fr & 1 ? odd[e] : even[e];
+            own[(h * TP + j) * 64 + w.lane] = v;
         }
-        barrier_lds_only();
     }
+    barrier_lds_only();
+    const int j = (w.wave - a.it) & (MOE_WAVES - 1);   // another wave from item to item
+    if (j < TP && 2 * j < a.groups) {
+        const int row = a.r0 + 8 * (2 * j + (w.fr & 1)) + (w.fr >> 1);
+        v4f t[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            t[h] = (v4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int v = 0; v < MOE_WAVES; v++) t[h] += ((const v4f *)slot_of<ST>(v))[(h * TP + j) * 64 + w.lane];
+        }
+        float v[4] = {t[0][0], t[0][1], t[0][2], t[0][3]};
+        act_all(v, g.act);
+        if (row < a.n) {
+            typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+            v4bf hi, lo;
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const float h = v[q] * t[1][q];
+                hi[q] = (__bf16)h;
+                lo[q] = (__bf16)(h - (float)hi[q]);
+            }
+            uint16_t *to = g.h + ((int64_t)(w.l->at[a.first + row] >> 8) * g.I + a.c0) * 2 + 4 * w.fg;
+            *(v4bf *)to = hi;
+            *(v4bf *)(to + 16) = lo;
+        }
+    }
+    barrier_lds_only();
 }
 
 // One stage, in slot ST, the next one's loads first.  False after the last.
@@ -770,7 +782,7 @@ __device__ __forceinline__ bool up_stage(v4f (&acc)[2][G], UpRegs<G> (&r)[2], Up
                                          const UpWork &w, const MoeArgs &g, const LaneOffsets<2> &o) {
     up_load<G, ST ^ 1>(r[ST ^ 1], next, w, g, o);
     wait_stage<2, G>(next.groups);
-    const int units = min(w.end - (w.first + a.k * SU<2>), SU<2>);
+    const int units = units_of<2>(a, w);
 #pragma unroll
     for (int q = 0; q < SU<2>; q++) {
         if (q >= units) break;
@@ -778,7 +790,7 @@ __device__ __forceinline__ bool up_stage(v4f (&acc)[2][G], UpRegs<G> (&r)[2], Up
         for (int h = 0; h < 2; h++) {
             v8bf wb[2];
             slot_frag<ST, 2>(wb, h, q, w.wave, w.fr, w.fg);
-            const float scale = lane_value(r[ST].sc, 8 * h + q);
+            const float scale = lane_value(r[ST].sc, h);
 #pragma unroll
             for (int i = 0; i < G; i++) {
                 if (i >= a.groups) break;
@@ -811,22 +823,32 @@ __global__ void __launch_bounds__(MOE_NT) moe_up_kernel(MoeArgs g) {
     w.x = make_rsrc(g.x, g.M * g.D * 2);
     w.blocks = (int)(g.I / 16);
     w.items = uniform(l.count) * w.blocks;
-    const int units = (int)(g.D / 64);
-    w.stages = stages_of<2>(units);
-    w.first = share(units, w.wave);
-    w.end = share(units, w.wave + 1);
+    const int blocks = (int)(g.D / 128);
+    w.stages = stages_of<2>(blocks);
+    w.first = share(blocks, w.wave);
+    w.end = share(blocks, w.wave + 1);
     const LaneOffsets<2> o = lane_offsets<2>((int)g.D, w.lane);
     UpAt<G> a = {};
     a.it = blockIdx.x;
     if (a.it >= w.items) return;
     up_item<G>(a, w, g.D);
-    UpAt<G> next = a;
-    UpRegs<G> r[2];
     v4f acc[2][G];
 #pragma unroll
     for (int h = 0; h < 2; h++)
 #pragma unroll
         for (int i = 0; i < G; i++) acc[h][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+    if (w.first == w.end) {   // no share: its part in the others' sums
+        for (int stage = 0; a.it < w.items; stage++) {
+            if (a.k == w.stages - 1) {
+                if (stage & 1) up_finish<G, 1>(acc, a, w, g);
+                else up_finish<G, 0>(acc, a, w, g);
+            }
+            up_next<G>(a, w, g.D);
+        }
+        return;
+    }
+    UpAt<G> next = a;
+    UpRegs<G> r[2];
     up_load<G, 0>(r[0], next, w, g, o);
     up_next<G>(next, w, g.D);
     while (up_stage<G, 0>(acc, r, a, next, w, g, o) && up_stage<G, 1>(acc, r, a, next, w, g, o)) {
@@ -894,7 +916,7 @@ __device__ __forceinline__ void down_load(DownRegs<T> &r, const DownAt &a, const
                                           const LaneOffsets<T> &o) {
     const int64_t row = (int64_t)a.expert * g.D + w.n0;
     const int u0 = w.first + a.k * SU<T>;
-    const int units = a.n > 0 ? min(max(w.end - u0, 0), SU<T>) : 0;
+    const int units = units_of<T>(a, w);
 #pragma unroll
     for (int i = 0; i < DG; i++) {
         if (i >= a.groups) break;
@@ -920,7 +942,7 @@ __device__ __forceinline__ bool down_stage(v4f (&acc)[T][DG], DownRegs<T> (&r)[2
                                            const DownWork &w, const MoeArgs &g, const LaneOffsets<T> &o) {
     down_load<T, ST ^ 1>(r[ST ^ 1], next, w, g, o);
     wait_stage<T, DG>(next.groups);
-    const int units = min(w.end - (w.first + a.k * SU<T>), SU<T>);
+    const int units = units_of<T>(a, w);
 #pragma unroll
     for (int q = 0; q < SU<T>; q++) {
         if (q >= units) break;
@@ -988,13 +1010,13 @@ __global__ void __launch_bounds__(MOE_NT) moe_down_kernel(MoeArgs g) {
     w.h = make_rsrc(g.h, (int64_t)g.M * g.topk * g.I * 4);
     w.count = uniform(l.count);
     w.n0 = (int64_t)blockIdx.x * 16 * T;
-    const int units = (int)(g.I / 64);
-    w.stages = stages_of<T>(units);
-    w.first = share(units, w.wave);
-    w.end = share(units, w.wave + 1);
+    const int blocks = (int)(g.I / 128);
+    w.stages = stages_of<T>(blocks);
+    w.first = share(blocks, w.wave);
+    w.end = share(blocks, w.wave + 1);
     const LaneOffsets<T> o = lane_offsets<T>((int)g.I, w.lane);
     DownAt a = {};
-    if (w.count > 0) {
+    if (w.count > 0 && w.first < w.end) {
         down_item(a, w, g.I);
         DownAt next = a;
         DownRegs<T> r[2];
