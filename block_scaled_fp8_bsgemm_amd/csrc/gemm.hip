@@ -908,7 +908,7 @@ __device__ __forceinline__ void store_tile(const v4f (&acc)[TM][TN], const GemmA
 // are gate columns in the order that brow_of gives them, and 2 and 3 the up columns of
 // the same ones, a lane holds both of each of its 8 columns and the product stays in
 // its registers.
-enum { EPI_NONE, EPI_ACT, EPI_GLU };
+enum { EPI_NONE, EPI_ACT, EPI_RESID, EPI_GLU };   // EPI_RESID: EPI_ACT with a residual
 
 struct ActArgs {
     const uint16_t *bias;    // bf16 [N] (GLU: [2 N]) or null
@@ -963,15 +963,18 @@ __device__ __forceinline__ u32x4 load_resid8(const ActArgs &q, int64_t at) {
 // A tile's accumulators in place of their results (GLU: in sub-tiles 0 and 1).  The
 // residual comes in the pieces of the store (tile_pieces), whole 128-byte row segments,
 // BATCH row groups at a time, and goes to its columns' lanes by the same exchange.  Four
-// at a time: M = 16384, N = 7168, K = 2048 with a residual 266 us, against 270 for eight and
-// 273 for two, and 235 without bias, activation and residual.  What is left is the read of
-// the residual after the products, 235 MB or 44 us at the rate of a large copy, of which 13
-// are behind the tiles of other CUs.
-template <bool GLU, int BATCH>
+// at a time: M = 16384, N = 7168, K = 2048 with a residual 256 to 268 us on one card or
+// another, 1 % and 2 % less than with eight and two, against 229 to 236 without bias, activation
+// and residual.  What is left is the read of the residual after the products, 235 MB or 44 us
+// at the rate of a large copy, of which about a third is behind the tiles of other CUs.  Half of it by
+// DMA into the free stage during the last K block took 276 for 264 (264 non-temporal), and one
+// kernel with and without a residual 264 for 256.
+template <int EPI, int BATCH>
 __device__ __forceinline__ void act_tile(v4f (&acc)[TM][TN], const GemmArgs &g, const ActArgs &q, int64_t m0,
-                                         int64_t n0, int wm, int wn, int lane) {
+                                         int64_t n0, int wave, int lane) {
+    constexpr bool GLU = EPI == EPI_GLU;
     asm volatile("" : "+v"(lane));   // addresses formed here, not hoisted
-    const int frow = lane & 15, fg = lane >> 4;
+    const int wm = wave >> 2, wn = wave & 3, frow = lane & 15, fg = lane >> 4;
     const bool up = (lane >> 3) & 1;
     const int64_t n = n0 + wn * (GLU ? 32 : 64);
     if (n >= g.N) return;   // N % 128 == 0: all of the wave's columns
@@ -981,18 +984,18 @@ __device__ __forceinline__ void act_tile(v4f (&acc)[TM][TN], const GemmArgs &g, 
 #pragma unroll
     for (int h = 0; h < TM; h += BATCH) {
         u32x4 r[BATCH][2] = {};
-        if (q.resid) {
+        if (EPI == EPI_RESID || (GLU && q.resid)) {
 #pragma unroll
-            for (int i = 0; i < BATCH; i++) {
-                r[i][0] = load_resid8(q, band_at(g, o, (h + i) * 16, 0));
-                if (!GLU) r[i][1] = load_resid8(q, band_at(g, o, (h + i) * 16 + 8, up ? -32 : 32));
-            }
+            for (int i = 0; i < BATCH; i++)
+#pragma unroll
+                for (int y = 0; y < (GLU ? 1 : 2); y++)
+                    r[i][y] = load_resid8(q, band_at(g, o, (h + i) * 16 + 8 * y, y ? (up ? -32 : 32) : 0));
         }
 #pragma unroll
         for (int i = 0; i < BATCH; i++) {
             v4f(&c)[TN] = acc[h + i];
             u32x4 ra = r[i][0], rb = r[i][1];
-            if (q.resid && !GLU) {
+            if (EPI == EPI_RESID) {
                 ra = up ? r[i][1] : r[i][0];
                 rb = swap_rows8(up ? r[i][0] : r[i][1]);
             }
@@ -1383,7 +1386,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const LoraGemmArgs 
     if constexpr (LORA) {
         if (any) lora_add(acc, g, q, m0, n0 + wn * WN, wm, wave, lane);
     }
-    if constexpr (EPI != EPI_NONE) act_tile<GLU, 4>(acc, g, ep, m0, n0, wm, wn, lane);
+    if constexpr (EPI != EPI_NONE) act_tile<EPI, 4>(acc, g, ep, m0, n0, wave, lane);
     if constexpr (GLU) store_gated_tile(acc, g, m0, n0, wave, lane);
     else store_tile<MODE>(acc, g, m0, n0, wave, lane);
 }
@@ -1677,7 +1680,7 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
                 ActKArgs ka = (ActKArgs)gp;
                 asm volatile("" : "+s"(ka));
                 const ActGemmArgs at = *(const ActGemmArgs *)ka;
-                act_tile<GLU, 2>(acc, at.g, at.q, m0, n0, wm, wn, lane);
+                act_tile<EPI, 2>(acc, at.g, at.q, m0, n0, wave, lane);
             }
             const bool plain = tile_is_plain<COLS>(args(), m0, n0);
             if (!has_next || !plain) {
@@ -2426,8 +2429,9 @@ int bs_launch_gemm_act(const uint8_t *A, const float *sa, const uint8_t *B, cons
     if (gated && g.KB % 2 == 0 && (M + BM) * K <= lim && (2 * N + BN) * K <= lim)
         return bs_enqueue(bsgemm_act_persistent_kernel<EPI_GLU>, dim3(persistent_grid(g, stream)), dim3(NTHREADS), stream, a);
     const dim3 grid(gemm_grid(g));
-    return gated ? bs_enqueue(bsgemm_act_tile_kernel<EPI_GLU>, grid, dim3(NTHREADS), stream, a)
-                 : bs_enqueue(bsgemm_act_tile_kernel<EPI_ACT>, grid, dim3(NTHREADS), stream, a);
+    return gated   ? bs_enqueue(bsgemm_act_tile_kernel<EPI_GLU>, grid, dim3(NTHREADS), stream, a)
+           : resid ? bs_enqueue(bsgemm_act_tile_kernel<EPI_RESID>, grid, dim3(NTHREADS), stream, a)
+                   : bs_enqueue(bsgemm_act_tile_kernel<EPI_ACT>, grid, dim3(NTHREADS), stream, a);
 }
 
 int bs_launch_gemm_pb(const uint8_t *A, const float *sa, const uint8_t *Bp, const float *sb,
