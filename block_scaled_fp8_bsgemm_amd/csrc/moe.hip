@@ -26,6 +26,10 @@ namespace {
 // order compares lie closer than what fp32 may be off (route_close), it is chosen again by
 // fp64 keys.  That happens to about one row in a hundred of 256 experts with random
 // logits; an fp64 exponential for every expert took as long as all the rest.
+//
+// The selection's instructions bound it, about 900 a row: 16384 rows of 256 experts, sigmoid,
+// bias, 4 of 8 groups, 8 experts 23 us (17.8 MB; all by fp64 keys 45), 3001 rows of 60 experts by
+// their logits 4.0, 64 rows of 256 with groups 8.8 if one of them needs fp64 keys, else 5.
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ int dpp_from(int old, int v) {
@@ -397,14 +401,22 @@ __global__ void __launch_bounds__(256) moe_route_kernel(RouteArgs g) {
 // bf16 (hi + lo, 17 bits), and a weight's e4m3 code is a bf16 value exactly.  Products
 // are bf16 MFMAs with fp32 sums, one scale for each 64 deep piece of a 128 x 128 block.
 //
-//   moe_up    a workgroup to a CU; an item is one expert, 16 columns of W1 and the same
+//   moe_up    two workgroups to a CU; an item is one expert, 16 columns of W1 and the same
 //             of W3.  The waves split D, and their sums are added in wave order
-//   moe_down  a workgroup: 16 columns of out; an item is one expert, in ascending
-//             order.  The waves split I; each has its own sums for every token, weighted,
-//             and these are added in wave order at the end
+//   moe_down  a workgroup: 16 or 32 columns of out and one class of the experts; an item is
+//             one of them, in ascending order.  The waves split I; each has its own sums for
+//             every token, weighted, and these are added in wave order at the end
+//   moe_join  with more classes than one: their sums, in order
 //
 // How D and I are split does not depend on the tokens, so a token's result is the
 // same in every batch, and no sum depends on timing.
+//
+// Measured, up / down, D = 7168, I = 2048: one token of 8 experts 43.9 / 25.1 us (5.3 and 4.7
+// TB/s), 16 tokens of 64 experts, 8 each, 278 / 147 (6.0 and 5.6), 128 tokens of 32 experts here of
+// 256 165 / 120 (5.7 and 3.9: their sums fill LDS, so the workgroups have 16 columns, and 448 of
+// them share 256 CUs).  Reading the experts' rows and nothing else reaches 6.2 TB/s, in any
+// pattern of 128 bytes or more; 64-byte pieces a fifth less.  5 tokens of 16 experts of 1024 x 384,
+// 7.0 / 7.7 and 2.6 to join: making the lists takes 2, a round of loads 1, an item's sums 1.
 //
 // The weights come by DMA into two slots of LDS for each wave, 32 rows x 128 bytes (or 16 x
 // 256) to a slot, and the other operand to registers, also for one slot ahead: a wave multiplies
@@ -1083,7 +1095,11 @@ int bs_launch_moe_route(RouteArgs g, hipStream_t stream) {
 }
 
 // Classes that the experts are split into by their numbers, each with workgroups of its
-// own: with few columns the workgroups are few, and each takes about 1 us an expert.
+// own: with few columns the workgroups are few, and each takes about 1 us an expert.  In all,
+// without / with: 40 tokens of 59 experts, D = 128, I = 384 102 / 33 us; 5 tokens of 16, 1024 x 384
+// 21.3 / 16.2; 16 tokens of 64, 4096 x 1536 260 / 206; but one token of 2 of 16, 1024 x 512 13.7 /
+// 14.4 (the join is a launch of 3 us).  Half as many classes 33, 17.6, 260; twice as many 33, 16.1,
+// 213, and at D = 7168, where one is enough, 441 against 428 for 16 tokens of 64 experts.
 constexpr int CLASS_COLUMNS = 8192;   // about 256 workgroups of 32 columns
 static int moe_classes(int64_t E, int64_t D) {
     const int64_t most = (E + 1) / 2, c = CLASS_COLUMNS / D;   // two experts to a class

@@ -39,7 +39,7 @@
  *                in its epilogue
  *   moe_route    each token's experts and their weights, from the router's logits
  *   moe_fp8      the experts of a few tokens: both products, the gated activation
- *                and the weighted sum, in two kernels
+ *                and the weighted sum, in two or three kernels
  *
  * Pages defining the operations (cited by title and section):
  *   [PR40757] sglang PR 40757 "[AMD][gfx950] DSV4: fuse wo_b's GEMM with its
@@ -422,7 +422,7 @@ bs_status lora_expand(const float *H, const uint16_t *B, const float *scale, con
  * 255 / 328; strewn over 4 adapters 331 / 336, 8: 413 / 338, 32: 733 / 341, 128: 1329 /
  * 348; R = 16 over 4: 269 / 312, 8: 312 / 315, 32: 412 / 316; R = 128 over 2: 347 / 373,
  * 4: 457 / 373; 1024 rows, R = 64, over 4: 39 / 39, 32: 86 / 57; 200 rows, R = 64, over
- * 4: 18 / 34, 128: 48 / 52.
+ * 4: 16 / 34, 128: 46 / 52.
  *
  *   A, a_scale, B, b_scale, C, bands, band_stride  as for bsgemm_fp8
  *   H           fp32 [M, R], from lora_shrink
@@ -563,11 +563,12 @@ bs_status moe_route(const void *logits, const float *bias, int32_t *ids, float *
  * expert of another GPU, whose sum is added across GPUs); a row of empty slots is base,
  * or zero.  An expert named twice by a row counts once, with the sum of the two weights.
  * Weights are e4m3 values with 128 x 128 fp32 scales; x is not quantized, and h is
- * carried to 2^-17 (within bf16's largest value).  A row's result does not depend on the other rows or their number,
- * and a value that is not finite, in a row or in an expert that it uses, reaches no
- * other row.
+ * carried to 2^-17 (within bf16's largest value).  A row's result does not depend on the
+ * other rows or their number, and a value that is not finite, in a row or in an expert
+ * that it uses, reaches no other row.
  *
- * Two kernels, bound by reading the weights of the experts in use once.
+ * Two kernels, three where D is at most 4096 and E more than 2, bound by reading the
+ * weights of the experts in use once.
  *
  *   x        bf16 [M, D];  ids  int32 [M, topk];  weights  fp32 [M, topk]
  *   W13      e4m3 [E, 2I, D];  s13  fp32 [E, 2I/128, D/128]
