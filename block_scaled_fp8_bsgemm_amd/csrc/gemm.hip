@@ -860,7 +860,8 @@ __device__ __forceinline__ bool tile_is_plain(const GemmArgs &g, int64_t m0, int
     return m0 + BM <= g.M && n0 + COLS <= g.N && g.band_stride == g.band_rows * g.N;
 }
 
-template <int MODE>
+// WIDE: rows may be more than 2^24 elements long.
+template <int MODE, bool WIDE = true>
 __device__ __forceinline__ void store_tile(const v4f (&acc)[TM][TN], const GemmArgs &g, int64_t m0,
                                            int64_t n0, int wave, int lane) {
     // opaque to the compiler, so that the addresses below are formed here
@@ -870,9 +871,9 @@ __device__ __forceinline__ void store_tile(const v4f (&acc)[TM][TN], const GemmA
     const bool up = (lane >> 3) & 1;                 // r >= 8
     const int px = (lane >> 4) + (up ? 4 : 0);       // piece of the X store
     const int dny = up ? -32 : 32;                   // the Y store's piece, in columns from X's
-    if (tile_is_plain(g, m0, n0)) {
+    if ((!WIDE || g.N <= (int64_t)1 << 24) && tile_is_plain(g, m0, n0)) {
         // row-major C, no bounds: a uniform base per row group and one
-        // 32-bit lane offset (the tile spans 256 rows of N <= 2^22 elements)
+        // 32-bit lane offset (rows 0 .. 143 of N elements)
         const uint32_t lx = (uint32_t)((wm * WM + (lane & 7)) * g.N + wn * WN + px * 8);
         const uint32_t ly = lx + (uint32_t)(8 * g.N + dny);
         uint16_t *base = g.C + m0 * g.N + n0;
@@ -1653,7 +1654,7 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
             // drain under the next tile's first K block, whose block 0 and
             // head are already in.
             const bool plain = tile_is_plain(args(), m0, n0);
-            if (!has_next || !plain) store_tile<MODE>(acc, args(), m0, n0, wave, lane);
+            if (!has_next || !plain) store_tile<MODE, false>(acc, args(), m0, n0, wave, lane);
             if (!has_next) break;
             {
                 const GemmArgs gt = args();
@@ -1685,7 +1686,7 @@ __device__ __forceinline__ void gemm_persistent(const GemmArgs &g) {
             const bool plain = tile_is_plain<COLS>(args(), m0, n0);
             if (!has_next || !plain) {
                 if constexpr (GLU) store_gated_tile(acc, args(), m0, n0, wave, lane);
-                else store_tile<MODE>(acc, args(), m0, n0, wave, lane);
+                else store_tile<MODE, false>(acc, args(), m0, n0, wave, lane);
             }
             if (!has_next) break;
             {
@@ -2417,8 +2418,9 @@ int bs_launch_gemm_act(const uint8_t *A, const float *sa, const uint8_t *B, cons
         if (M <= 32) return launch_act_rows<2>(a, gated, stream);
         if (rows4 <= 256) return launch_act_rows<4>(a, gated, stream);
     }
-    if (M <= MID_BM || count(MID_BM, mid_cols) <= 512) {
-        const dim3 grid((unsigned)((count(MID_BM, mid_cols) + NUM_XCD - 1) / NUM_XCD * NUM_XCD));
+    const int64_t mid = count(MID_BM, mid_cols);
+    if (mid <= 512 || (M <= MID_BM && mid < (int64_t)1 << 23)) {   // fewer than 2^32 lanes
+        const dim3 grid((unsigned)((mid + NUM_XCD - 1) / NUM_XCD * NUM_XCD));
         return gated ? bs_enqueue(bsgemm_act_mid_kernel<true>, grid, dim3(NTHREADS), stream, a)
                      : bs_enqueue(bsgemm_act_mid_kernel<false>, grid, dim3(NTHREADS), stream, a);
     }

@@ -181,6 +181,7 @@ class FFNServeStep:
     number of rows, which need no z.  Experts: up to 128 rows.  The next resnorm takes out as
     its y.  z, q and q_scale may be refilled between steps: every buffer is allocated here
     and step() only enqueues, so it can be captured.
+    The router's plan is made here, once, on the current stream.
     """
 
     DENSE, ROUTED = ("up", "quantize", "down"), ("logits", "route", "experts")
@@ -243,5 +244,6 @@ class FFNServeStep:
                 act=self.act, out=self.out, ws=self.ws)
 
     def step(self):
-        for ph in self.PHASES:
-            getattr(self, ph)()
+        if self.out.shape[0]:
+            for ph in self.PHASES:
+                getattr(self, ph)()

@@ -242,3 +242,45 @@ def test_millions_of_columns():
         half = N // 2
         C = bs.bsgemm_fp8_act(A, sa, B, sb, gated=True).view(3, half)
         assert bool((C[0] == want[:half] * want[half:]).all())
+
+
+def test_rows_of_millions_of_columns():
+    """Whole tiles whose rows lie 2^25 elements apart, and the ragged ones below them."""
+    M, N, K = 300, 1 << 25, 128
+    A = torch.zeros((M, K), dtype=torch.uint8, device=device())
+    A[:, 5] = (torch.arange(M, device=device()) % 8).float().to(torch.float8_e4m3fn).view(torch.uint8)
+    B = torch.zeros((N, K), dtype=torch.uint8, device=device())
+    B[:, 5] = 0x38
+    sa = torch.ones((M, 1), dtype=torch.float32, device=device())
+    sb = (torch.arange(N // 128, device=device()) % 4 + 1).to(torch.float32).view(-1, 1)
+    cols = sb.view(-1).repeat_interleave(128).bfloat16()
+    for what in ("bsgemm_fp8", "bsgemm_fp8_act", "gated"):
+        say(f"300 rows of 2^25 columns: {what}")
+        if what == "bsgemm_fp8":
+            C = bs.bsgemm_fp8(A, sa, B, sb).view(M, N)
+        else:
+            C = bs.bsgemm_fp8_act(A, sa, B, sb, act="relu", gated=what == "gated").view(M, -1)
+        want = cols if what != "gated" else cols[: N // 2] * cols[N // 2:]
+        for m in (0, 1, 7, 100, 135, 142, 143, 144, 200, 255, 256, 299):
+            v = m % 8
+            assert bool((C[m] == want * (v * v if what == "gated" else v)).all()), (what, m)
+        del C
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_offsets_past_32_bits(gated):
+    """A past 2^31 bytes and C past 2^31 elements, in place on the residual."""
+    say(f"bsgemm_fp8_act 2^24 rows gated={gated}")
+    M, N, K = (1 << 24) + 77, 128, 128
+    row = torch.arange(M, device=device()) % 16
+    A = torch.zeros((M, K), dtype=torch.uint8, device=device())
+    A[:, 3] = row.float().to(torch.float8_e4m3fn).view(torch.uint8)
+    sa = torch.ones((M, 1), dtype=torch.float32, device=device())
+    rows = 256 if gated else 128
+    B = torch.zeros((rows, K), dtype=torch.uint8, device=device())
+    B[:, 3] = 0x38
+    sb = torch.ones((rows // 128, 1), dtype=torch.float32, device=device())
+    C = (torch.arange(M, device=device()) % 5).bfloat16().repeat_interleave(N)
+    bs.bsgemm_fp8_act(A, sa, B, sb, act="none", gated=gated, resid=C, alpha=2.0, C=C)
+    want = (row * row if gated else row) + 2 * (torch.arange(M, device=device()) % 5)
+    assert bool((C.view(M, N) == want.bfloat16()[:, None]).all())

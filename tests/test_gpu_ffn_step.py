@@ -163,6 +163,14 @@ def test_steps_follow_their_stream():
             assert torch.equal(a, b)
 
 
+def test_empty_batch():
+    say("feed-forward step without rows")
+    s = make(M=0)
+    s.step()
+    torch.cuda.synchronize()
+    assert s.out.shape == (0, 512) and s.ids.shape == (0, 4)
+
+
 # ------------------------------------------------------------ the calls --
 
 def random_codes(shape, g):

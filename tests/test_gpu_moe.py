@@ -113,6 +113,15 @@ def test_route_no_rows_and_many():
     assert bool(((w.double() - s / s.sum(1, keepdim=True)).abs() <= 2.0 ** -23).all())
 
 
+def test_route_more_rows_than_a_launch_holds():
+    say("moe_route 2^25 + 5 rows")
+    M = (1 << 25) + 5
+    x = torch.zeros((M, 2), dtype=torch.bfloat16, device=device())
+    x[:, 1] = (torch.arange(M, device=device()) % 3 - 1).bfloat16()
+    ids, w = run_route(x, 1)
+    assert bool((ids[:, 0] == (x[:, 1] > 0)).all()) and bool((w == 1).all())
+
+
 # ---------------------------------------------------------------- experts --
 
 def make(M, E, topk, D, I, seed=0, mix="distinct", heavy=False):
