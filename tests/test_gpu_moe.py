@@ -169,7 +169,8 @@ def run_moe(x, ids, w, W13, s13, W2, s2, base=None, act="silu", inplace=False):
 
 MOE = [(1, 1, 1, 128, 128), (1, 32, 8, 1024, 512), (5, 16, 2, 384, 640), (16, 8, 4, 256, 384), (17, 4, 2, 512, 256),
        (33, 3, 2, 128, 384), (64, 12, 8, 256, 128), (100, 1, 1, 128, 1152), (128, 6, 3, 384, 128), (128, 40, 8, 128, 256),
-       (2, 70, 64, 128, 128), (16, 1000, 64, 128, 128), (3, 5, 3, 7168, 128), (3, 5, 3, 128, 2048)]
+       (2, 70, 64, 128, 128), (16, 1000, 64, 128, 128), (3, 5, 3, 7168, 128), (3, 5, 3, 128, 2048),
+       (1, 9, 8, 256, 384), (4, 3, 2, 384, 128), (8, 4, 1, 128, 256), (2, 30, 4, 512, 384), (3, 4, 3, 128, 128)]
 
 
 @pytest.mark.parametrize("M,E,topk,D,I", MOE)
