@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(256) moe_route_kernel(RouteArgs g) {
 // How D and I are split does not depend on the tokens, so a token's result is the
 // same in every batch, and no sum depends on timing.
 //
-// Measured, up / down, D = 7168, I = 2048: one token of 8 experts 43.9 / 25.1 us (5.3 and 4.7
+// Measured, up / down, D = 7168, I = 2048: one token of 8 experts 44.0 / 24.3 us (5.3 and 4.8
 // TB/s), 16 tokens of 64 experts, 8 each, 278 / 147 (6.0 and 5.6), 128 tokens of 32 experts here of
 // 256 165 / 120 (5.7 and 3.9: their sums fill LDS, so the workgroups have 16 columns, and 448 of
 // them share 256 CUs).  Reading the experts' rows and nothing else reaches 6.2 TB/s, in any
@@ -1145,7 +1145,7 @@ int bs_launch_moe_route(RouteArgs g, hipStream_t stream) {
 // own: with few columns the workgroups are few, and each takes about 1 us an expert.  In all,
 // without / with: 40 tokens of 59 experts, D = 128, I = 384 102 / 33 us; 5 tokens of 16, 1024 x 384
 // 21.3 / 16.2; 16 tokens of 64, 4096 x 1536 260 / 206; but one token of 2 of 16, 1024 x 512 13.7 /
-// 14.4 (the join is a launch of 3 us).  Half as many classes 33, 17.6, 260; twice as many 33, 16.1,
+// 14.4 (the join is a launch of 3 us; 12.7 since few_lists).  Half as many classes 33, 17.6, 260; twice as many 33, 16.1,
 // 213, and at D = 7168, where one is enough, 441 against 428 for 16 tokens of 64 experts.
 constexpr int CLASS_COLUMNS = 8192;   // about 256 workgroups of 32 columns
 static int moe_classes(int64_t E, int64_t D) {
