@@ -2336,14 +2336,20 @@ static int persistent_grid(const GemmArgs &g, hipStream_t stream) {
     return grid < per ? grid : per;
 }
 
+// Whether the persistent kernels take a product: they address each operand through one
+// descriptor with 31-bit lane offsets, the rows of a ragged last tile included, and a whole
+// tile's rows of C through another, past whose 2^31 bytes a store is dropped (N = 4210688
+// is the widest).
+static bool persistent_fits(const GemmArgs &g, int64_t rows_of_B) {
+    const int64_t lim = 0x7FFFFFFF;
+    return g.KB % 2 == 0 && (g.M + BM) * g.K <= lim && (rows_of_B + BN) * g.K <= lim && ((BM - 1) * g.N + BN) * 2 <= lim;
+}
+
 int bs_launch_gemm(const uint8_t *A, const float *sa, const uint8_t *B, const float *sb,
                    uint16_t *C, int64_t M, int64_t N, int64_t K, int64_t band_rows,
                    int64_t band_stride, hipStream_t stream) {
     const GemmArgs g = gemm_args(A, sa, B, sb, C, M, N, K, band_rows, band_stride);
-    // The persistent kernel addresses each operand through one descriptor
-    // with 31-bit lane offsets, the rows of a ragged last tile included.
-    const int64_t lim = 0x7FFFFFFF;
-    if (g.KB % 2 == 0 && (M + BM) * K <= lim && (N + BN) * K <= lim)
+    if (persistent_fits(g, N))
         return bs_enqueue(bsgemm_persistent_kernel, dim3(persistent_grid(g, stream)), dim3(NTHREADS),
                           stream, g);
     return bs_enqueue(bsgemm_tile_kernel, dim3(gemm_grid(g)), dim3(NTHREADS), stream, g);
@@ -2427,8 +2433,7 @@ int bs_launch_gemm_act(const uint8_t *A, const float *sa, const uint8_t *B, cons
     // The gated epilogue fits beside the persistent kernel's carried products (M = 16384,
     // N = 2048: K = 2048 125 us against the tile kernel's 131, K = 7168 426 against 429); the
     // plain one, with twice the columns to a lane, spilled 38 to 86 registers there.
-    const int64_t lim = 0x7FFFFFFF;   // as for bsgemm_fp8
-    if (gated && g.KB % 2 == 0 && (M + BM) * K <= lim && (2 * N + BN) * K <= lim)
+    if (gated && persistent_fits(g, 2 * N))
         return bs_enqueue(bsgemm_act_persistent_kernel<EPI_GLU>, dim3(persistent_grid(g, stream)), dim3(NTHREADS), stream, a);
     const dim3 grid(gemm_grid(g));
     return gated   ? bs_enqueue(bsgemm_act_tile_kernel<EPI_GLU>, grid, dim3(NTHREADS), stream, a)
@@ -2455,8 +2460,7 @@ int bs_launch_mxgemm(const uint8_t *A, const uint8_t *sa, const uint8_t *B, cons
                      uint16_t *C, int64_t M, int64_t N, int64_t K, int64_t band_rows,
                      int64_t band_stride, hipStream_t stream) {
     const GemmArgs g = gemm_args(A, sa, B, sb, C, M, N, K, band_rows, band_stride);
-    const int64_t lim = 0x7FFFFFFF;   // as for the blockscale kernel
-    if (g.KB % 2 == 0 && (M + BM) * K <= lim && (N + BN) * K <= lim)
+    if (persistent_fits(g, N))
         return bs_enqueue(mxgemm_persistent_kernel, dim3(persistent_grid(g, stream)), dim3(NTHREADS),
                           stream, g);
     return bs_enqueue(mxgemm_tile_kernel, dim3(gemm_grid(g)), dim3(NTHREADS), stream, g);
