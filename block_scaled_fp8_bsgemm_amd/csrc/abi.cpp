@@ -38,6 +38,12 @@ inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.h
 
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// Whether one launch holds the products' tiles of 256 x 256, 512 lanes to each: their number
+// is rounded up to a multiple of the 8 XCDs, and the lanes stay fewer than 2^32.
+inline bool tiles_fit(int64_t M, int64_t rows_of_B) {
+    return (M + 255) / 256 * ((rows_of_B + 255) / 256) <= ((int64_t)1 << 23) - 8;
+}
+
 inline hipStream_t as_stream(void *s) { return (hipStream_t)s; }
 
 }  // namespace
@@ -69,7 +75,7 @@ bs_status blockscale_gemm(Launch launch, More more, const uint8_t *A, const floa
     if (!A || !a_scale || !B || !b_scale || !C) return BS_ERR_INVALID;
     if (M < 0 || N <= 0 || K <= 0 || bands < 1 || band_stride < 0) return BS_ERR_INVALID;
     if (N % 128 || K % 128 || bands > 64) return BS_ERR_UNSUPPORTED;
-    if (M >= kMaxDim || N >= kMaxDim || K > kMaxK) return BS_ERR_UNSUPPORTED;
+    if (M >= kMaxDim || N >= kMaxDim || K > kMaxK || !tiles_fit(M, N)) return BS_ERR_UNSUPPORTED;
     if (M % bands) return BS_ERR_UNSUPPORTED;
     const int64_t band_rows = M / bands;
     const int64_t stride = band_stride == 0 ? band_rows * N : band_stride;
@@ -129,7 +135,7 @@ bs_status mxgemm_fp8(const uint8_t *A, const uint8_t *a_scale, const uint8_t *B,
     if (!A || !a_scale || !B || !b_scale || !C) return BS_ERR_INVALID;
     if (M < 0 || N <= 0 || K <= 0 || bands < 1 || band_stride < 0) return BS_ERR_INVALID;
     if (N % 128 || K % 128 || bands > 64) return BS_ERR_UNSUPPORTED;
-    if (M >= kMaxDim || N >= kMaxDim || K > kMaxK) return BS_ERR_UNSUPPORTED;
+    if (M >= kMaxDim || N >= kMaxDim || K > kMaxK || !tiles_fit(M, N)) return BS_ERR_UNSUPPORTED;
     if (M % bands) return BS_ERR_UNSUPPORTED;
     const int64_t band_rows = M / bands;
     const int64_t stride = band_stride == 0 ? band_rows * N : band_stride;
@@ -358,7 +364,7 @@ bs_status bsgemm_fp8_act(const uint8_t *A, const float *a_scale, const uint8_t *
     if (!std::isfinite(alpha) || !std::isfinite(beta)) return BS_ERR_INVALID;
     if (N > 0 && N < kMaxDim && M > 0 && M < kMaxDim) {
         const int64_t rows = gated ? 2 * N : N;   // of B
-        if (rows >= kMaxDim || (M + 255) / 256 * ((rows + 255) / 256) >= ((int64_t)1 << 23)) return BS_ERR_UNSUPPORTED;
+        if (rows >= kMaxDim || !tiles_fit(M, rows)) return BS_ERR_UNSUPPORTED;
     }
     if (!aligned(bias, 16) || !aligned(resid, 16)) return BS_ERR_UNSUPPORTED;
     const auto more = [&](Range rc) {

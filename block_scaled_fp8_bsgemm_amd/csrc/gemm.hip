@@ -2424,9 +2424,9 @@ int bs_launch_gemm_act(const uint8_t *A, const float *sa, const uint8_t *B, cons
         if (M <= 32) return launch_act_rows<2>(a, gated, stream);
         if (rows4 <= 256) return launch_act_rows<4>(a, gated, stream);
     }
-    const int64_t mid = count(MID_BM, mid_cols);
-    if (mid <= 512 || (M <= MID_BM && mid < (int64_t)1 << 23)) {   // fewer than 2^32 lanes
-        const dim3 grid((unsigned)((mid + NUM_XCD - 1) / NUM_XCD * NUM_XCD));
+    const int64_t mid = count(MID_BM, mid_cols), mid_grid = (mid + NUM_XCD - 1) / NUM_XCD * NUM_XCD;
+    if (mid <= 512 || (M <= MID_BM && lanes_fit(mid_grid, NTHREADS))) {
+        const dim3 grid((unsigned)mid_grid);
         return gated ? bs_enqueue(bsgemm_act_mid_kernel<true>, grid, dim3(NTHREADS), stream, a)
                      : bs_enqueue(bsgemm_act_mid_kernel<false>, grid, dim3(NTHREADS), stream, a);
     }

@@ -107,13 +107,17 @@ int bs_stream_cus(hipStream_t stream);   // CUs of the stream's device
 
 #include <tuple>
 
+// Whether one dimension of a launch holds so many workgroups of so many lanes.
+inline bool lanes_fit(int64_t workgroups, int64_t lanes) { return workgroups * lanes < (int64_t)1 << 32; }
+
 // Enqueue `kernel` with hipLaunchKernel and report that launch's own status
 // (not a sticky error left by an unrelated earlier call).  No dimension may hold 2^32
 // lanes or more: the runtime refuses that or, seen too, runs their number modulo
-// 2^32 and reports success.
+// 2^32 and reports success; so it is refused here.
 template <typename... KArgs, typename... Args>
 int bs_enqueue(void (*kernel)(KArgs...), dim3 grid, dim3 block, hipStream_t stream, Args... args) {
     static_assert(sizeof...(KArgs) == sizeof...(Args), "kernel argument count");
+    if (!(lanes_fit(grid.x, block.x) && lanes_fit(grid.y, block.y) && lanes_fit(grid.z, block.z))) return -1;
     std::tuple<KArgs...> a(args...);
     hipError_t rc = hipSuccess;
     std::apply(

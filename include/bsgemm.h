@@ -126,7 +126,8 @@ typedef enum {
  * Requirements: M >= 0 (M = 0 is a no-op); N > 0 and N % 128 == 0;
  * K > 0 and K % 128 == 0; 1 <= bands <= 64 and M % bands == 0;
  * band_stride == 0 or band_stride >= band_rows * N; A, B and C 16-byte
- * aligned, a_scale and b_scale 4-byte aligned; C must not overlap any input.
+ * aligned, a_scale and b_scale 4-byte aligned; C must not overlap any input;
+ * K <= 2^22, M and N below 2^31, and at most 2^23 - 8 tiles of 256 x 256.
  * Violations: null pointers, negative sizes, bands < 1 or overlap ->
  * BS_ERR_INVALID; the rest -> BS_ERR_UNSUPPORTED.  M need not be a multiple
  * of the tile: ragged rows are handled in the kernel.
@@ -286,7 +287,7 @@ bs_status bsgemm_fp8_pb(const uint8_t *A, const float *a_scale,
  * Requirements: M >= 0; N > 0, N % 128 == 0; K > 0, K % 128 == 0, K <= 2^22;
  * bands in [1, 64] dividing M; band_stride 0 or >= (M/bands)*N and a multiple
  * of 8; A, B, C 16-byte aligned; a_scale, b_scale 4-byte aligned; C must not
- * overlap an input.
+ * overlap an input; M and N below 2^31, and at most 2^23 - 8 tiles of 256 x 256.
  */
 bs_status mxgemm_fp8(const uint8_t *A, const uint8_t *a_scale,
                      const uint8_t *B, const uint8_t *b_scale,
@@ -503,9 +504,8 @@ bs_status resnorm(const void *y, const float *y_scale, const void *resid, const 
  *   resid       bf16, in bands as C (bands, band_stride), or null; may be C itself
  *   C           bf16 bands of M x N
  *
- * Requirements: those of bsgemm_fp8, with 2N for N where B's rows count; fewer than
- * 2^23 tiles of 256 rows of A by 256 of B; alpha and beta finite; bias and resid
- * 16-byte aligned; C must not overlap an input, except resid == C.
+ * Requirements: those of bsgemm_fp8, with 2N for N where B's rows count; alpha and beta
+ * finite; bias and resid 16-byte aligned; C must not overlap an input, except resid == C.
  */
 typedef enum {
     BS_ACT_NONE = 0,
