@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(256) moe_route_kernel(RouteArgs g) {
     if (g.renorm) {
         double sum = w;
         for (int off = 1; off < g.topk; off <<= 1) sum += __shfl_xor(sum, off, 64);
-        w = sum == 0.0 ? 0.0 : w / sum;
+        w = mine < 0 || sum == 0.0 ? 0.0 : w / sum;   // an empty slot's beside a sum of NaN, too
     }
     if (live) {
         g.ids[(row0 + r) * g.topk + k] = mine;
