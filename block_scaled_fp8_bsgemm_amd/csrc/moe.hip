@@ -84,13 +84,17 @@ __device__ __forceinline__ float unordered(int k) { return __builtin_bit_cast(fl
 
 __device__ __forceinline__ int first_lane(uint64_t lanes) { return __ffsll((unsigned long long)lanes) - 1; }
 
-// Whether two keys, or sums of two, may be in the other order by fp64.  The hardware's
-// exponential of a is off by (2 a + 2) 2^-24 relative, a < 104.  A sigmoid plus a bias is so
-// off by less than 2^-21 (1 + |key|), since s (1 - s) a < 1/4; a score without bias by less
-// than 2^-16 of itself; and the margins are over four times as much for either two.
+// Whether two keys, or sums of two, a that fp32 puts first and b, may be in the other order
+// by fp64.  An exponential e^-t by the hardware's and its reciprocal are off by (3 t + 5)
+// 2^-24 relative, and softmax's sum by less than 50 2^-24.  So with a bias a sigmoid is off by
+// less than 2^-21, all softmax scores together by less than 2^-18, and the key's own rounding is
+// 2^-24 of it; the margin is twice as much for either two.  Without one a score is off by
+// less than 2^-16 of itself, an eighth of the margin, but only where it is a normal number:
+// the hardware gives zero below 2^-126, off by all of its value.  So nothing up to 2^-100 is
+// decided here; above that a sum's lost second key is 2^-26 of it.
 __device__ __forceinline__ bool route_close(float a, float b, bool biased) {
     const float margin = biased ? 0x1p-17f * (1.0f + fabsf(a) + fabsf(b)) : 0x1p-13f * (a + b);
-    return !(a - b > margin);
+    return !(a - b > margin) || (!biased && a <= 0x1p-100f);
 }
 
 // The largest and second largest key of group `lane`, by way of LDS.
