@@ -241,6 +241,7 @@ __device__ __forceinline__ int choose_f32(const float (&x)[EPL], const RouteArgs
             group_best(lds, g, lane, KEY_NONE, best, second);
         }
         int score = best == KEY_NONE ? KEY_NONE : group_score(best, second, g);
+        const int sum = score;
         const int own = whole ? lane & -lanes : lane;   // the first lane of the lane's group
         uint64_t keep = 0;
         for (; k < g.topk_groups; k++) {
@@ -251,7 +252,20 @@ __device__ __forceinline__ int choose_f32(const float (&x)[EPL], const RouteArgs
             if (own == l) score = KEY_NONE;
             last = m;
         }
-        if (k == g.topk_groups) {
+        // The last kept and the first left out decide.  But a sum of two keys of either sign is
+        // off by what they are, which may be far more than the sum and another from group to
+        // group; then the least that any kept sum can be lies above the most that any other can.
+        const bool pair = g.group_top == 2 && second != KEY_NONE;
+        if (biased && __ballot(pair && best >= 0 && second < 0)) {
+            const float mag = best == KEY_NONE ? 0.f : fabsf(unordered(best)) + (pair ? fabsf(unordered(second)) : 0.f);
+            const float off = 0x1p-18f * (1.0f + mag), v = unordered(sum);
+            const bool kept = keep >> own & 1;
+            // an infinite bound decides nothing, nor does one that is not a number
+            const int least = kept ? ordered(off < INFINITY ? -v + off : INFINITY) : KEY_NONE;
+            const int most = kept || sum == KEY_NONE ? KEY_NONE : ordered(off < INFINITY ? v + off : INFINITY);
+            const int l = wave_max(least), h = wave_max(most);
+            if (h != KEY_NONE && !(-unordered(l) > unordered(h))) ok = false;
+        } else if (k == g.topk_groups) {
             m = wave_max(score);
             if (m != KEY_NONE && route_close(unordered(last), unordered(m), biased)) ok = false;
         }
