@@ -22,14 +22,17 @@ __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcp
 // x / (1 + 2^-y)
 __device__ __forceinline__ float logistic_of(float x, float y) { return x * rcp_fast(1.0f + exp2_fast(-y)); }
 
+// No sum of a product is left to the compiler to fuse or not, which it would choose for
+// each kernel by itself: a row's result is the same in all of them.
 template <int ACT>
 __device__ __forceinline__ float act_one(float x) {
+#pragma clang fp contract(off)
     constexpr float LOG2E = 1.44269504f;
     if constexpr (ACT == ACT_RELU) return x < 0.0f ? 0.0f : x;
     if constexpr (ACT == ACT_SILU) return logistic_of(x, x * LOG2E);
     if constexpr (ACT == ACT_GELU_TANH) {
         constexpr float C = 2.0f * 0.797884561f * LOG2E;   // 2 sqrt(2/pi) log2(e)
-        return logistic_of(x, x * (C + C * 0.044715f * (x * x)));
+        return logistic_of(x, x * __builtin_fmaf(C * 0.044715f, x * x, C));
     }
     if constexpr (ACT == ACT_GELU) {
         // erfc(a / sqrt 2) = e^(-a^2/2) t P(t), t = 1 / (1 + 0.44 a / sqrt 2), a = |x|: P is
@@ -37,7 +40,7 @@ __device__ __forceinline__ float act_one(float x) {
         // is least (1.9e-7), fitted to erfc's values.  No cancellation: for x < 0 the
         // result is x/2 erfc, for x >= 0 it is x - x/2 erfc with erfc <= 1.
         const float a = __builtin_fabsf(x);
-        const float t = rcp_fast(1.0f + 0.311126977f * a);
+        const float t = rcp_fast(__builtin_fmaf(0.311126977f, a, 1.0f));
         float p = 0.0714833736f;
         p = __builtin_fmaf(p, t, -0.279080987f);
         p = __builtin_fmaf(p, t, 0.298737288f);
@@ -46,8 +49,8 @@ __device__ __forceinline__ float act_one(float x) {
         p = __builtin_fmaf(p, t, 0.21695715f);
         p = __builtin_fmaf(p, t, 0.248931631f);
         p = __builtin_fmaf(p, t, 0.248216793f);
-        const float half_erfc = 0.5f * (p * t) * exp2_fast(x * x * (-0.5f * LOG2E));
-        return x * (x < 0.0f ? half_erfc : 1.0f - half_erfc);
+        const float h = 0.5f * (p * t), e = exp2_fast(x * x * (-0.5f * LOG2E));   // half erfc: h e
+        return x * (x < 0.0f ? h * e : __builtin_fmaf(-h, e, 1.0f));
     }
     return x;
 }

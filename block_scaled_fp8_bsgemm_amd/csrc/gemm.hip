@@ -931,15 +931,15 @@ __device__ __forceinline__ void add8(float (&t)[8], u32x4 b) {
         t[2 * e + 1] += bf16_hi(b[e]);
     }
 }
-__device__ __forceinline__ void join8(float (&v)[8], u32x4 r, const ActArgs &q) {
+// N values v: alpha r + beta v, rounded after beta v and once more, or beta v.
+template <int N, typename Bits>
+__device__ __forceinline__ void join(float (&v)[N], Bits r, const ActArgs &q) {
+#pragma clang fp contract(off)
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-        v[2 * e] = q.beta * v[2 * e];
-        v[2 * e + 1] = q.beta * v[2 * e + 1];
-        if (q.resid) {
-            v[2 * e] += q.alpha * bf16_lo(r[e]);
-            v[2 * e + 1] += q.alpha * bf16_hi(r[e]);
-        }
+    for (int e = 0; e < N; e++) v[e] = q.beta * v[e];
+    if (q.resid) {
+#pragma unroll
+        for (int e = 0; e < N; e++) v[e] = __builtin_fmaf(q.alpha, e & 1 ? bf16_hi(r[e >> 1]) : bf16_lo(r[e >> 1]), v[e]);
     }
 }
 __device__ __forceinline__ u32x4 load_bias8(const ActArgs &q, int64_t n) {
@@ -1013,7 +1013,7 @@ __device__ __forceinline__ void act_tile(v4f (&acc)[TM][TN], const GemmArgs &g, 
 #pragma unroll
                 for (int e = 0; e < 8; e++) v[e] *= u[e];
             }
-            join8(v, ra, q);
+            join(v, ra, q);
 #pragma unroll
             for (int e = 0; e < 8; e++) c[e >> 2][e & 3] = v[e];
             if constexpr (!GLU) {
@@ -1021,7 +1021,7 @@ __device__ __forceinline__ void act_tile(v4f (&acc)[TM][TN], const GemmArgs &g, 
                 for (int e = 0; e < 8; e++) v[e] = c[2 + (e >> 2)][e & 3];
                 add8(v, b1);
                 act_all(v, q.act);
-                join8(v, rb, q);
+                join(v, rb, q);
 #pragma unroll
                 for (int e = 0; e < 8; e++) c[2 + (e >> 2)][e & 3] = v[e];
             }
@@ -2123,18 +2123,16 @@ __global__ void __launch_bounds__(NTHREADS) bsgemm_act_mid_kernel(ActGemmArgs a)
             float v[4] = {t[0], t[1], t[2], t[3]};
             act_all(v, q.act);
 #pragma unroll
-            for (int e = 0; e < 4; e++) v[e] *= q.beta * t[4 + e];
-            if (q.resid) {
-                const u32x2 r = *(const u32x2 *)(q.resid + at);
-                v[0] += q.alpha * bf16_lo(r[0]); v[1] += q.alpha * bf16_hi(r[0]);
-                v[2] += q.alpha * bf16_lo(r[1]); v[3] += q.alpha * bf16_hi(r[1]);
-            }
+            for (int e = 0; e < 4; e++) v[e] *= t[4 + e];
+            u32x2 r = {0u, 0u};
+            if (q.resid) r = *(const u32x2 *)(q.resid + at);
+            join(v, r, q);
             *(u32x2 *)(g.C + at) = (u32x2){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         } else {
             act_all(t, q.act);
             u32x4 r = {0u, 0u, 0u, 0u};
             if (q.resid) r = *(const u32x4 *)(q.resid + at);
-            join8(t, r, q);
+            join(t, r, q);
             *(u32x4 *)(g.C + at) = pack8(t);
         }
     }
@@ -2259,11 +2257,9 @@ __global__ void __launch_bounds__(NTHREADS) bsgemm_act_rows_kernel(ActGemmArgs a
         u32x2 r = {0u, 0u};
         if (q.resid) r = *(const u32x2 *)(q.resid + at);
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
+        for (int e = 0; e < 4; e++)
             if (GLU) v[e] *= u[e];
-            v[e] *= q.beta;
-            if (q.resid) v[e] += q.alpha * (e & 1 ? bf16_hi(r[e >> 1]) : bf16_lo(r[e >> 1]));
-        }
+        join(v, r, q);
         *(u32x2 *)(g.C + at) = (u32x2){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     }
 }
