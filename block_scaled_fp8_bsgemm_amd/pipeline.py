@@ -202,6 +202,11 @@ class FFNServeStep:
             raise ValueError("the experts need z")
         M, D = (q if z is None else z).shape
         dev = (q if z is None else z).device
+        if dense is not None:   # what the calls cannot see: each would write a part of its buffer alone
+            I = dense[2].shape[1]
+            for name, t, shape in (("q", q, (M, D)), ("dense B13", dense[0], (2 * I, D)), ("dense B2", dense[2], (D, I))):
+                if tuple(t.shape) != shape:
+                    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
 
         def new(shape, dtype):
             return torch.empty(shape, dtype=dtype, device=dev)
@@ -211,7 +216,6 @@ class FFNServeStep:
         self.out = new((M, D), torch.bfloat16)
         self.PHASES = (self.DENSE if dense is not None else ()) + (self.ROUTED if experts is not None else ())
         if dense is not None:
-            I = dense[2].shape[1]
             self.h = new((M, I), torch.bfloat16)
             self.hq, self.h_scale = new((M, I), torch.uint8), new((M, I // 128), torch.float32)
         if experts is not None:
