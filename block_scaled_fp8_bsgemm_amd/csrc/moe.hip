@@ -93,8 +93,8 @@ __device__ __forceinline__ int first_lane(uint64_t lanes) { return __ffsll((unsi
 // the hardware gives zero below 2^-126, off by all of its value.  So nothing up to 2^-100 is
 // decided here; above that a sum's lost second key is 2^-26 of it.
 __device__ __forceinline__ bool route_close(float a, float b, bool biased) {
-    const float margin = biased ? 0x1p-17f * (1.0f + fabsf(a) + fabsf(b)) : 0x1p-13f * (a + b);
-    return !(a - b > margin) || (!biased && a <= 0x1p-100f);
+    const float part = biased ? 0x1p-17f : 0x1p-13f, least = biased ? 0x1p-17f : 0x1p-100f;
+    return !(a - b > __builtin_fmaf(part, fabsf(a) + fabsf(b), least));
 }
 
 // The largest and second largest key of group `lane`, by way of LDS.
@@ -241,7 +241,6 @@ __device__ __forceinline__ int choose_f32(const float (&x)[EPL], const RouteArgs
             group_best(lds, g, lane, KEY_NONE, best, second);
         }
         int score = best == KEY_NONE ? KEY_NONE : group_score(best, second, g);
-        const int sum = score;
         const int own = whole ? lane & -lanes : lane;   // the first lane of the lane's group
         uint64_t keep = 0;
         for (; k < g.topk_groups; k++) {
@@ -256,13 +255,13 @@ __device__ __forceinline__ int choose_f32(const float (&x)[EPL], const RouteArgs
         // off by what they are, which may be far more than the sum and another from group to
         // group; then the least that any kept sum can be lies above the most that any other can.
         const bool pair = g.group_top == 2 && second != KEY_NONE;
-        if (biased && __ballot(pair && best >= 0 && second < 0)) {
+        if (biased && __ballot(pair && (best ^ second) < 0)) {
             const float mag = best == KEY_NONE ? 0.f : fabsf(unordered(best)) + (pair ? fabsf(unordered(second)) : 0.f);
-            const float off = 0x1p-18f * (1.0f + mag), v = unordered(sum);
+            const float off = 0x1p-18f * (1.0f + mag), v = unordered(group_score(best, second, g));
             const bool kept = keep >> own & 1;
             // an infinite bound decides nothing, nor does one that is not a number
             const int least = kept ? ordered(off < INFINITY ? -v + off : INFINITY) : KEY_NONE;
-            const int most = kept || sum == KEY_NONE ? KEY_NONE : ordered(off < INFINITY ? v + off : INFINITY);
+            const int most = kept || best == KEY_NONE ? KEY_NONE : ordered(off < INFINITY ? v + off : INFINITY);
             const int l = wave_max(least), h = wave_max(most);
             if (h != KEY_NONE && !(-unordered(l) > unordered(h))) ok = false;
         } else if (k == g.topk_groups) {
