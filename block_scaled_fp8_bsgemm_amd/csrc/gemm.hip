@@ -1713,10 +1713,9 @@ __global__ void __launch_bounds__(NTHREADS) bsgemm_persistent_kernel(GemmArgs g)
     if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8)) gemm_persistent<MODE_BS, 1>(g);
     else gemm_persistent<MODE_BS, 0>(g);
 }
-template <int EPI>
 __global__ void __launch_bounds__(NTHREADS) bsgemm_act_persistent_kernel(ActGemmArgs a) {
-    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8)) gemm_persistent<MODE_BS, 1, EPI>(a.g);
-    else gemm_persistent<MODE_BS, 0, EPI>(a.g);
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8)) gemm_persistent<MODE_BS, 1, EPI_GLU>(a.g);
+    else gemm_persistent<MODE_BS, 0, EPI_GLU>(a.g);
 }
 __global__ void __launch_bounds__(NTHREADS) mxgemm_persistent_kernel(GemmArgs g) {
     gemm_persistent<MODE_MX, -1>(g);
@@ -1961,12 +1960,6 @@ __device__ __forceinline__ void mid_load(const MidLoader &L, int kb) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(L.rS, (lds_void *)(st + (MID_BM + MID_BN) * BK + L.wave * 256), 4, L.offS,
                                              kb * 4, 0, 0);
 }
-
-// A wave's operands of one K block, in registers.
-struct MidBlock {
-    v8i a[2], b[2];
-    float s[2][2];
-};
 
 // b_scale of the K blocks from `first` on, one to a lane (of gate and up columns).
 // Loaded at each block they come between the blocks' DMA, and waiting for them is
@@ -2430,7 +2423,7 @@ int bs_launch_gemm_act(const uint8_t *A, const float *sa, const uint8_t *B, cons
     // N = 2048: K = 2048 125 us against the tile kernel's 131, K = 7168 426 against 429); the
     // plain one, with twice the columns to a lane, spilled 38 to 86 registers there.
     if (gated && persistent_fits(g, 2 * N))
-        return bs_enqueue(bsgemm_act_persistent_kernel<EPI_GLU>, dim3(persistent_grid(g, stream)), dim3(NTHREADS), stream, a);
+        return bs_enqueue(bsgemm_act_persistent_kernel, dim3(persistent_grid(g, stream)), dim3(NTHREADS), stream, a);
     const dim3 grid(gemm_grid(g));
     return gated   ? bs_enqueue(bsgemm_act_tile_kernel<EPI_GLU>, grid, dim3(NTHREADS), stream, a)
            : resid ? bs_enqueue(bsgemm_act_tile_kernel<EPI_RESID>, grid, dim3(NTHREADS), stream, a)
