@@ -568,7 +568,8 @@ bs_status moe_route(const void *logits, const float *bias, int32_t *ids, float *
  * that it uses, reaches no other row.
  *
  * Two kernels, three where D is at most 4096 and E more than 2, bound by reading the
- * weights of the experts in use once.
+ * weights of the experts in use: W13[e] once for each 32 and W2[e] for each 16 of an
+ * expert's tokens.
  *
  *   x        bf16 [M, D];  ids  int32 [M, topk];  weights  fp32 [M, topk]
  *   W13      e4m3 [E, 2I, D];  s13  fp32 [E, 2I/128, D/128]
